@@ -25,10 +25,11 @@ STATUS_NAMES = {
     4: "DUO_ERR_WORKSPACE", 5: "DUO_ERR_CUDA", 6: "DUO_ERR_TIMEOUT",
     7: "DUO_ERR_UNSUPPORTED", 8: "DUO_ERR_STATE",
 }
-DUO_F32, DUO_BF16, DUO_INT4 = 0, 1, 2
+DUO_F32, DUO_BF16, DUO_INT4, DUO_FP8 = 0, 1, 2, 3
+FP8_BLOCK = 32
 DUO_LAYOUT_PACKED = 0
 DUO_LAYOUT_PAGED = 1
-KV_DTYPES = {"f32": DUO_F32, "bf16": DUO_BF16, "int4": DUO_INT4}
+KV_DTYPES = {"f32": DUO_F32, "bf16": DUO_BF16, "int4": DUO_INT4, "fp8": DUO_FP8}
 
 
 class DuoError(RuntimeError):
@@ -64,6 +65,18 @@ class duo_layout_view(ctypes.Structure):
                 ("pool_blocks", ctypes.c_int64), ("block_table", ctypes.c_int64)]
 
 
+class duo_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class duo_rope_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_float),
+                ("norm_eps", ctypes.c_float), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -81,6 +94,14 @@ SIGNATURES = {
     "duo_release_rows": (_I32, [_P, _P, _I32]),
     "duo_append_kv": (_I32, [_P, _I32, _P, _P, _I32, _P]),
     "duo_append_kv_rows": (_I32, [_P, _I32, _P, _I32, _P, _P, _I32, _P]),
+    "duo_qk_norm_rope": (_I32, [ctypes.POINTER(duo_rope_desc), _I32, _I64, _I32, _I32, _I32,
+                                ctypes.POINTER(duo_heads), ctypes.POINTER(duo_heads), _P, _P, _P, _P]),
+    "duo_append_rope": (_I32, [_P, _I32, ctypes.POINTER(duo_rope_desc), ctypes.POINTER(duo_heads),
+                               ctypes.POINTER(duo_heads), ctypes.POINTER(duo_heads), _P, _I32, _P, _P]),
+    "duo_append_rope_rows": (_I32, [_P, _I32, _P, _I32, ctypes.POINTER(duo_rope_desc),
+                                    ctypes.POINTER(duo_heads), ctypes.POINTER(duo_heads),
+                                    ctypes.POINTER(duo_heads), _P, _I32, _P, _P]),
+    "duo_fp8_tail_info": (_I32, [_P, _I32, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "duo_decode_attn": (_I32, [_P, _I32, _P, _P, _F, _P, _SZ, _P]),
     "duo_decode_attn_rows": (_I32, [_P, _I32, _P, _I32, _P, _P, _F, _P, _SZ, _P]),
     "duo_decode_step": (_I32, [_P, _I32, _P, _P, _P, _P, _F, _P, _SZ, _P]),
@@ -259,6 +280,35 @@ def duo_cache_reset(handle):
 
 def duo_append_kv(handle, layer, k_ptr, v_ptr, n_tokens, stream=0):
     _check(lib().duo_append_kv(handle, layer, k_ptr, v_ptr, n_tokens, stream), "duo_append_kv")
+
+
+def duo_qk_norm_rope(rope, dtype, n_tokens, n_q_heads, n_kv_heads, head_dim, q, k, positions_ptr,
+                     q_out_ptr, k_out_ptr, stream=0):
+    """rope: duo_rope_desc; q, k: duo_heads or None; dtype "bf16" or "f32"."""
+    _check(lib().duo_qk_norm_rope(rope, KV_DTYPES.get(dtype, dtype), n_tokens, n_q_heads, n_kv_heads,
+                                  head_dim, q, k, positions_ptr, q_out_ptr, k_out_ptr, stream),
+           "duo_qk_norm_rope")
+
+
+def duo_append_rope(handle, layer, rope, q, k, v, positions_ptr, n_tokens, q_out_ptr, stream=0):
+    """rope: duo_rope_desc; q (or None), k, v: duo_heads."""
+    _check(lib().duo_append_rope(handle, layer, rope, q, k, v, positions_ptr, n_tokens, q_out_ptr,
+                                 stream), "duo_append_rope")
+
+
+def duo_append_rope_rows(handle, layer, rows, rope, q, k, v, positions_ptr, n_tokens, q_out_ptr,
+                         stream=0):
+    arr, n = _rows(rows)
+    _check(lib().duo_append_rope_rows(handle, layer, arr, n, rope, q, k, v, positions_ptr, n_tokens,
+                                      q_out_ptr, stream), "duo_append_rope_rows")
+
+
+def duo_fp8_tail_info(handle, layer):
+    """Byte offsets (K, V) of an 8-bit cache layer's tail buffers; -1 where there are none."""
+    k, v = _I64(), _I64()
+    _check(lib().duo_fp8_tail_info(handle, layer, ctypes.byref(k), ctypes.byref(v)),
+           "duo_fp8_tail_info")
+    return k.value, v.value
 
 
 def duo_decode_attn(handle, layer, q_ptr, out_ptr, softmax_scale, ws_ptr, ws_bytes, stream=0):

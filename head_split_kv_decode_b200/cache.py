@@ -8,8 +8,10 @@ read and written by the library's kernels.
 import torch
 
 from . import binding as B
+from .rotary import heads_view, on_device
 
-_TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "int4": torch.bfloat16}
+_TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "int4": torch.bfloat16,
+                "fp8": torch.bfloat16}
 _ALIGN = 256
 
 
@@ -29,7 +31,8 @@ class DuoCache:
     """A head-split KV cache for ``layers`` layers bound to torch-allocated memory.
 
     head_mask: [layers, n_kv_heads] of 0/1 (1 = retrieval head).
-    kv_dtype: "f32", "bf16" or "int4" (K/V given in bf16 and quantised on append).
+    kv_dtype: "f32", "bf16", "int4" (K/V given in bf16 and quantised on append) or "fp8" (K/V given
+    in bf16; retrieval heads held as e4m3 with one scale per ``binding.FP8_BLOCK`` tokens).
     pool_blocks: None for the packed layout (``capacity`` tokens reserved per
     batch row), or the block count of the paged layout's retrieval pool
     (blocks of ``binding.PAGE_TOKENS`` tokens taken by rows as they grow;
@@ -66,7 +69,7 @@ class DuoCache:
         self._pf_ws, self.pf_ws_ptr = None, None
 
     def _prefill_ws(self):
-        """Pre-fill scratch (4-bit caches only), allocated on first use."""
+        """Pre-fill scratch (4-bit and 8-bit caches only), allocated on first use."""
         if self.prefill_ws_bytes == 0:
             return None, 0
         if self._pf_ws is None:
@@ -96,6 +99,51 @@ class DuoCache:
         self._check(v, shape, "v")
         B.duo_append_kv(self.handle, layer, k.data_ptr(), v.data_ptr(), n,
                         _stream_handle(stream, self.device))
+
+    def append_rope(self, layer, rotary, k, v, q=None, positions=None, q_out=None, stream=None):
+        """:meth:`append` with k normed and rotated on the way by ``rotary``
+        (:class:`.rotary.Rotary`), and q ([batch, n_tokens, n_q_heads,
+        head_dim]) too when given: returns the rotated queries (else None).
+
+        k, v and q may be strided views (slices of a projection's output) whose
+        (row, token) pairs lie at one stride; positions: int64 [batch,
+        n_tokens], default each token's place in its row.
+        """
+        return self._append_rope(layer, None, rotary, k, v, q, positions, q_out, stream)
+
+    def append_rope_rows(self, layer, rows, rotary, k, v, q=None, positions=None, q_out=None,
+                         stream=None):
+        """:meth:`append_rope` for the listed rows (leading dimension len(rows))."""
+        return self._append_rope(layer, self._rows(rows), rotary, k, v, q, positions, q_out, stream)
+
+    def _append_rope(self, layer, rows, rotary, k, v, q, positions, q_out, stream):
+        n_rows = self.batch if rows is None else len(rows)
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a [rows, n_tokens, n_kv_heads, head_dim] tensor")
+        n = k.shape[1]
+        if rotary.head_dim != self.head_dim:
+            raise ValueError("rotary is for head_dim %d, the cache's is %d"
+                             % (rotary.head_dim, self.head_dim))
+        desc = rotary.desc(self.io_dtype, self.device)
+        kv_shape = (n_rows, n, self.n_kv_heads, self.head_dim)
+        kh = heads_view(k, kv_shape, "k", self.io_dtype, self.device)
+        vh = heads_view(v, kv_shape, "v", self.io_dtype, self.device)
+        qh, qo_ptr, pos_ptr = None, None, None
+        with on_device(self.device, stream) as s:
+            if q is not None:
+                q_shape = (n_rows, n, self.n_q_heads, self.head_dim)
+                qh = heads_view(q, q_shape, "q", self.io_dtype, self.device)
+                if q_out is None:
+                    q_out = torch.empty(q_shape, dtype=self.io_dtype, device=self.device)
+                self._check(q_out, q_shape, "q_out")
+                qo_ptr = q_out.data_ptr()
+            elif q_out is not None:
+                raise ValueError("q_out without q")
+            if positions is not None:
+                self._check(positions, (n_rows, n), "positions", torch.int64)
+                pos_ptr = positions.data_ptr()
+            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh, kh, vh, pos_ptr, n, qo_ptr, s)
+        return q_out
 
     def decode(self, layer, q, out=None, scale=0.0, stream=None):
         """q: [batch, n_q_heads, head_dim] at position seq_len-1.  Returns out."""
@@ -271,32 +319,47 @@ class DuoCache:
     def region(self, layer, name):
         """Raw view of one buffer of one layer (for inspection and tests).
 
-        name in ret_k, ret_v, str_k, str_v (rows of K/V elements or int4 codes) and,
-        for int4, ret_k_sz, ret_v_sz, str_k_sz, str_v_sz (fp16 scale/zero pairs).
+        name in ret_k, ret_v, str_k, str_v (rows of K/V elements or codes) and,
+        for int4, ret_k_sz, ret_v_sz, str_k_sz, str_v_sz (fp16 scale/zero pairs),
+        for fp8, ret_k_sz, ret_v_sz (one float32 scale per FP8_BLOCK rows) and
+        tail_k, tail_v (bf16 rows of the unfinished blocks).
         Returns a uint8 tensor [batch, heads, rows, row_bytes] (or [..., 4]);
         paged retrieval buffers are [pool_blocks, heads, page_tokens, ...].
         """
         lv = self.layout(layer)
-        off = getattr(lv, name)
+        fp8 = self.kv_dtype == "fp8"
+        if name.startswith("tail"):
+            off = B.duo_fp8_tail_info(self.handle, layer)[name == "tail_v"]
+        else:
+            off = getattr(lv, name)
         if off < 0:
             return None
-        heads = lv.n_retrieval if name.startswith("ret") else lv.n_streaming
+        heads = lv.n_streaming if name.startswith("str") else lv.n_retrieval
         outer, rows = self.batch, (lv.capacity if name.startswith("ret") else lv.window_stride)
         if self.paged and name.startswith("ret"):
             outer, rows = lv.pool_blocks, lv.page_tokens
+        if name.startswith("tail"):
+            rows = B.FP8_BLOCK
+        elif fp8 and name.endswith("_sz"):
+            rows //= B.FP8_BLOCK
         width = 4 if name.endswith("_sz") else lv.row_bytes
+        if fp8 and not name.startswith("ret"):
+            width = 2 * self.head_dim
         nbytes = outer * heads * rows * width
         return self.storage[off:off + nbytes].view(outer, heads, rows, width)
 
     def gather_rows(self, layer, name, row, n):
         """The first n retrieval rows of one batch row, in position order, as
-        [heads, n, width] (packed: a slice; paged: through the block table)."""
+        [heads, n, width] (packed: a slice; paged: through the block table).
+        Rows of an 8-bit cache's scales stand for FP8_BLOCK tokens each."""
         reg = self.region(layer, name)
         if reg is None:
             return None
         if not self.paged:
             return reg[row, :, :n]
-        P = self.layout(layer).page_tokens
+        if n == 0:
+            return reg[0, :, :0]
+        P = reg.shape[2]
         blocks = self.row_blocks(row)
         parts = [reg[blk] for blk in blocks[:(n + P - 1) // P]]
         return torch.cat(parts, dim=1)[:, :n]

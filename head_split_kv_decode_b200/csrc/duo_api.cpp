@@ -7,7 +7,10 @@
 //                    paged  [pool_blocks][n_retrieval][DUO_PAGE_TOKENS][row]
 //   streaming K, V : [batch][n_streaming][S + R][row]
 //   int4 only      : (fp16 scale, fp16 zero) per row, same indexing, for each
-// row = head_dim elements (f32 / bf16) or head_dim/2 bytes of 4-bit codes.
+//   fp8 only       : one float32 scale per 32 retrieval rows, and bf16 tails
+//                    [batch][n_retrieval][32][row] (K, V) of the open blocks
+// row = head_dim elements (f32 / bf16), head_dim/2 bytes of 4-bit codes, or
+// (fp8) head_dim codes for retrieval heads and head_dim bf16 for streaming.
 // Paged: one block table [batch][ceil(capacity / DUO_PAGE_TOKENS)] of int32
 // after the layers; block ids are shared by all layers (logical block i of
 // row b holds positions [256 i, 256 i + 256) of that row in every layer).
@@ -27,12 +30,14 @@
 
 #include "../../include/duo.h"
 #include "kernels.h"
+#include "kv8.h"
 
 static_assert(DUO_MAX_KV_HEADS == duo::kMaxKvHeads, "head table size");
 static_assert(DUO_MAX_SPLITS == duo::kMaxSplits, "split limit");
 static_assert(DUO_DECODE_STATIC_SCRATCH_BYTES == (8u << 20), "static decode scratch size");
 static_assert(DUO_PAGE_TOKENS == duo::kPageTokens, "page size");
 static_assert(DUO_MAX_LAUNCH_ROWS == duo::kMaxLaunchRows, "rows per launch");
+static_assert(DUO_FP8 == duo::kFP8 && DUO_FP8_BLOCK == duo::kScaleBlock, "8-bit cache");
 
 struct duo_cache {
   duo_cache_desc desc;
@@ -45,6 +50,7 @@ struct duo_cache {
     duo::HeadTables h;
     int64_t off_ret_k, off_ret_v, off_str_k, off_str_v;
     int64_t off_ret_k_sz, off_ret_v_sz, off_str_k_sz, off_str_v_sz;
+    int64_t off_tail_k, off_tail_v;  // fp8: open scale blocks in bf16
     int64_t ret_rows;         // storage rows of each retrieval buffer
   };
   std::vector<Layer> layers;
@@ -59,7 +65,8 @@ struct duo_cache {
   size_t cache_bytes;
   size_t ws_bytes;
   int n_ret_max;
-  int row_bytes;
+  int row_bytes;              // retrieval rows
+  int str_row_bytes;          // streaming rows (other than row_bytes for fp8 only)
   uint8_t *base;
   int forced_splits;
   int64_t shard_lo, shard_hi;  // retrieval heads keep positions [lo, hi) (sequence shard)
@@ -96,9 +103,21 @@ int64_t ret_len(const duo_cache *c, int64_t n) {
   return std::max<int64_t>(0, std::min(n, c->shard_hi) - c->shard_lo);
 }
 
-bool mma_path(const duo_cache *c) {
-  const duo_cache_desc &d = c->desc;
-  return duo::decode_mma_supported(d.kv_dtype, d.head_dim, d.n_q_heads / d.n_kv_heads);
+bool is_fp8(const duo_cache *c) { return c->desc.kv_dtype == DUO_FP8; }
+
+// Configurations decoded on tensor cores: any launch rows, paged or packed.
+bool tensor_core_decode(const duo_cache_desc &d) {
+  const int G = d.n_q_heads / d.n_kv_heads;
+  return d.kv_dtype == DUO_FP8 ? duo::decode_fp8_supported(d.head_dim, G)
+                               : duo::decode_mma_supported(d.kv_dtype, d.head_dim, G);
+}
+
+bool mma_path(const duo_cache *c) { return tensor_core_decode(c->desc); }
+
+duo::TailPtrs tail_ptrs(const duo_cache *c, int layer) {
+  const auto &L = c->layers[layer];
+  if (L.off_tail_k < 0) return duo::TailPtrs{nullptr, nullptr};
+  return duo::TailPtrs{c->base + L.off_tail_k, c->base + L.off_tail_v};
 }
 
 duo::LayerPtrs layer_ptrs(const duo_cache *c, int layer) {
@@ -166,7 +185,9 @@ duo_status launch_status(cudaError_t e) {
 cudaError_t cached_decode_config(duo_cache *c, duo::DecodeConfig *out) {
   if (!c->have_cfg) {
     const duo_cache_desc &d = c->desc;
-    cudaError_t e = duo::decode_config(d.kv_dtype, d.head_dim, d.n_q_heads / d.n_kv_heads, &c->cfg);
+    const int G = d.n_q_heads / d.n_kv_heads;
+    cudaError_t e = is_fp8(c) ? duo::decode_fp8_config(G, &c->cfg)
+                              : duo::decode_config(d.kv_dtype, d.head_dim, G, &c->cfg);
     if (e != cudaSuccess) return e;
     c->have_cfg = true;
   }
@@ -249,7 +270,9 @@ int choose_str_pack(const duo_cache *c, int layer, const int32_t *lens, int nrow
                     const duo::DecodeConfig &cfg) {
   const auto &L = c->layers[layer];
   if (L.n_ret == 0 || L.n_str <= 1 || c->forced_splits > 0) return 1;
-  const int64_t win_t = (win + 15) / 16 * 16;  // rows of the window's tiles of 16 keys
+  // rows of the window's tiles of 16 keys; next to 8-bit retrieval keys a
+  // bf16 streaming key weighs two
+  const int64_t win_t = (win + 15) / 16 * 16 * (is_fp8(c) ? 2 : 1);
   int best = 1;
   int64_t best_ctas = -1;
   int16_t ns[duo::kMaxLaunchRows];
@@ -378,7 +401,9 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
   if (d.layers <= 0 || d.batch <= 0 || d.n_q_heads <= 0 || d.n_kv_heads <= 0) return DUO_ERR_ARG;
   if (d.n_kv_heads > DUO_MAX_KV_HEADS || d.n_q_heads % d.n_kv_heads) return DUO_ERR_LAYOUT;
   if (d.head_dim != 64 && d.head_dim != 128) return DUO_ERR_ARG;
-  if (d.kv_dtype != DUO_F32 && d.kv_dtype != DUO_BF16 && d.kv_dtype != DUO_INT4) return DUO_ERR_ARG;
+  if (d.kv_dtype != DUO_F32 && d.kv_dtype != DUO_BF16 && d.kv_dtype != DUO_INT4 &&
+      d.kv_dtype != DUO_FP8)
+    return DUO_ERR_ARG;
   if (d.capacity <= 0 || d.capacity > INT32_MAX - duo::kPageTokens || S < 0 || R < 1)
     return DUO_ERR_ARG;
   for (int64_t i = 0; i < (int64_t)d.layers * d.n_kv_heads; ++i)
@@ -386,9 +411,9 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
   const bool paged = layout == DUO_LAYOUT_PAGED;
   if (paged) {
     if (pool_blocks <= 0 || pool_blocks > INT32_MAX) return DUO_ERR_ARG;
-    if (!duo::decode_mma_supported(d.kv_dtype, d.head_dim, d.n_q_heads / d.n_kv_heads))
-      return DUO_ERR_UNSUPPORTED;
+    if (!tensor_core_decode(d)) return DUO_ERR_UNSUPPORTED;
   }
+  if (d.kv_dtype == DUO_FP8 && !tensor_core_decode(d)) return DUO_ERR_UNSUPPORTED;
 
   duo_cache *c = new (std::nothrow) duo_cache();
   if (!c) return DUO_ERR_ARG;
@@ -403,7 +428,8 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
   // 4-bit: whole 16-byte groups of (scale, zero) rows, and whole 128-key
   // pre-fill tiles per packed retrieval head, so that a tile of the bf16
   // expansion never reaches into the next head's rows
-  if (d.kv_dtype == DUO_INT4) c->desc.capacity = round_up(d.capacity, 128);
+  // 8-bit: likewise (whole scale blocks too)
+  if (d.kv_dtype == DUO_INT4 || d.kv_dtype == DUO_FP8) c->desc.capacity = round_up(d.capacity, 128);
   c->mask.assign(head_mask, head_mask + (size_t)d.layers * d.n_kv_heads);
   c->seq_len.assign((size_t)d.layers * d.batch, 0);
   c->base = nullptr;
@@ -415,9 +441,11 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
   c->stall_ns = 0;
   c->have_cfg = false;
   c->row_bytes = d.kv_dtype == DUO_INT4 ? d.head_dim / 2 : d.head_dim * elem_bytes(d.kv_dtype);
+  c->str_row_bytes = c->row_bytes;
+  if (d.kv_dtype == DUO_FP8) c->row_bytes = d.head_dim;  // streaming rows stay bf16
   c->pool_blocks = paged ? pool_blocks : 0;
   c->table_stride = paged ? (int)((c->desc.capacity + duo::kPageTokens - 1) / duo::kPageTokens) : 0;
-  const bool q4 = d.kv_dtype == DUO_INT4;
+  const bool q4 = d.kv_dtype == DUO_INT4, q8 = d.kv_dtype == DUO_FP8;
 
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -445,12 +473,16 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
     const int64_t str_rows = (int64_t)d.batch * L.n_str * c->Ws;
     L.off_ret_k = L.n_ret ? take(L.ret_rows * c->row_bytes) : -1;
     L.off_ret_v = L.n_ret ? take(L.ret_rows * c->row_bytes) : -1;
-    L.off_str_k = L.n_str ? take(str_rows * c->row_bytes) : -1;
-    L.off_str_v = L.n_str ? take(str_rows * c->row_bytes) : -1;
-    L.off_ret_k_sz = (q4 && L.n_ret) ? take(L.ret_rows * 4) : -1;
-    L.off_ret_v_sz = (q4 && L.n_ret) ? take(L.ret_rows * 4) : -1;
+    L.off_str_k = L.n_str ? take(str_rows * c->str_row_bytes) : -1;
+    L.off_str_v = L.n_str ? take(str_rows * c->str_row_bytes) : -1;
+    const int64_t sz_bytes = q8 ? L.ret_rows / duo::kScaleBlock * 4 : L.ret_rows * 4;
+    L.off_ret_k_sz = ((q4 || q8) && L.n_ret) ? take(sz_bytes) : -1;
+    L.off_ret_v_sz = ((q4 || q8) && L.n_ret) ? take(sz_bytes) : -1;
     L.off_str_k_sz = (q4 && L.n_str) ? take(str_rows * 4) : -1;
     L.off_str_v_sz = (q4 && L.n_str) ? take(str_rows * 4) : -1;
+    const int64_t tail = (int64_t)d.batch * L.n_ret * duo::kScaleBlock * d.head_dim * 2;
+    L.off_tail_k = (q8 && L.n_ret) ? take(tail) : -1;
+    L.off_tail_v = (q8 && L.n_ret) ? take(tail) : -1;
     if (L.n_ret > c->n_ret_max) c->n_ret_max = L.n_ret;
     c->layers.push_back(L);
   }
@@ -469,14 +501,8 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
 
 // ---------------------------------------------------------------- append
 
-duo_status append_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &rows,
-                       const void *k, const void *v, int32_t n_tokens, cudaStream_t s) {
-  if (n_tokens < 0) return DUO_ERR_ARG;
-  if (n_tokens > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return DUO_ERR_ARG;
-  duo_status st = check_room(c, layer, rows, n_tokens);
-  if (st != DUO_OK) return st;
-  if (n_tokens == 0) return DUO_OK;  // k and v are not read (may be NULL)
-  if ((st = reserve_blocks(c, layer, rows, n_tokens, s)) != DUO_OK) return st;
+// Fields of an append that do not depend on its rows.
+duo::AppendParams append_params(const duo_cache *c, int32_t layer, int32_t n_tokens) {
   const auto &L = c->layers[layer];
   const duo_cache_desc &d = c->desc;
   duo::AppendParams a{};
@@ -494,21 +520,108 @@ duo_status append_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
   a.n_tok = n_tokens;
   a.shard_lo = c->shard_lo;
   a.shard_hi = c->shard_hi;
+  return a;
+}
+
+// Up to DUO_MAX_LAUNCH_ROWS of `rows` from g0 on, with their lengths.
+void fill_launch_rows(const duo_cache *c, int layer, const std::vector<int32_t> &rows, size_t g0,
+                      duo::LaunchRows *out) {
+  out->n = (int)std::min<size_t>(duo::kMaxLaunchRows, rows.size() - g0);
+  for (int r = 0; r < out->n; ++r) {
+    out->row[r] = rows[g0 + r];
+    out->len[r] = (int32_t)len_of(c, layer, rows[g0 + r]);
+  }
+}
+
+duo::HeadView view_at(const duo_heads *h, int64_t tok, int elt) {
+  if (!h) return duo::HeadView{nullptr, 0, 0};
+  return duo::HeadView{static_cast<const uint8_t *>(h->data) + tok * h->token_stride * elt,
+                       h->token_stride, h->head_stride};
+}
+
+// Append with the rotation (rope; null: none), each launch's queries to
+// q_out.  Arguments are checked; blocks are reserved here.
+duo_status append_rope_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &rows,
+                            const duo::RopeParams *rope, const duo_heads *q, const duo_heads *k,
+                            const duo_heads *v, const int64_t *positions, int32_t n_tokens,
+                            void *q_out, cudaStream_t s) {
+  duo_status st;
+  if ((st = reserve_blocks(c, layer, rows, n_tokens, s)) != DUO_OK) return st;
+  const duo_cache_desc &d = c->desc;
+  const int elt = elem_bytes(d.kv_dtype);
+  duo::RopeRowsParams p{};
+  if (rope) p.rope = *rope;
+  p.Hq = d.n_q_heads;
+  p.Hkv = d.n_kv_heads;
+  p.a = append_params(c, layer, n_tokens);
+  p.tail = tail_ptrs(c, layer);
+  for (size_t g0 = 0; g0 < rows.size(); g0 += duo::kMaxLaunchRows) {
+    fill_launch_rows(c, layer, rows, g0, &p.a.rows);
+    const int64_t tok = (int64_t)g0 * n_tokens;
+    p.tokens = (int64_t)p.a.rows.n * n_tokens;
+    p.q = view_at(q, tok, elt);
+    p.k = view_at(k, tok, elt);
+    p.v = view_at(v, tok, elt);
+    if (q_out) p.q_out = static_cast<uint8_t *>(q_out) + tok * d.n_q_heads * d.head_dim * elt;
+    if (positions) p.positions = positions + tok;
+    if ((st = launch_status(duo::launch_append_rope(p, d.kv_dtype, s))) != DUO_OK) return st;
+  }
+  for (int b : rows) len_of(c, layer, b) += n_tokens;
+  return DUO_OK;
+}
+
+duo_status append_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &rows,
+                       const void *k, const void *v, int32_t n_tokens, cudaStream_t s) {
+  if (n_tokens < 0) return DUO_ERR_ARG;
+  if (n_tokens > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return DUO_ERR_ARG;
+  duo_status st = check_room(c, layer, rows, n_tokens);
+  if (st != DUO_OK) return st;
+  if (n_tokens == 0) return DUO_OK;  // k and v are not read (may be NULL)
+  const duo_cache_desc &d = c->desc;
+  if (is_fp8(c)) {
+    const int64_t tok = (int64_t)d.n_kv_heads * d.head_dim;
+    const duo_heads kh{k, tok, d.head_dim}, vh{v, tok, d.head_dim};
+    return append_rope_rows(c, layer, rows, nullptr, nullptr, &kh, &vh, nullptr, n_tokens, nullptr, s);
+  }
+  if ((st = reserve_blocks(c, layer, rows, n_tokens, s)) != DUO_OK) return st;
+  duo::AppendParams a = append_params(c, layer, n_tokens);
   // inputs [rows][n_tokens][Hkv][D] in f32 (f32 caches) or bf16
   const int64_t in_row = (int64_t)n_tokens * d.n_kv_heads * d.head_dim * elem_bytes(d.kv_dtype);
   for (size_t g0 = 0; g0 < rows.size(); g0 += duo::kMaxLaunchRows) {
-    const int nr = (int)std::min<size_t>(duo::kMaxLaunchRows, rows.size() - g0);
-    a.rows.n = nr;
-    for (int r = 0; r < nr; ++r) {
-      a.rows.row[r] = rows[g0 + r];
-      a.rows.len[r] = (int32_t)len_of(c, layer, rows[g0 + r]);
-    }
+    fill_launch_rows(c, layer, rows, g0, &a.rows);
     a.k = static_cast<const uint8_t *>(k) + (int64_t)g0 * in_row;
     a.v = static_cast<const uint8_t *>(v) + (int64_t)g0 * in_row;
     if ((st = cuda_status(duo::launch_append(a, d.kv_dtype, s))) != DUO_OK) return st;
   }
   for (int b : rows) len_of(c, layer, b) += n_tokens;
   return DUO_OK;
+}
+
+// The rotation's description, checked and translated.
+duo_status rope_params(const duo_rope_desc *r, int32_t head_dim, duo::RopeParams *out) {
+  if (!r) return DUO_ERR_ARG;
+  if (r->rot_dim < 0 || r->rot_dim > head_dim || r->rot_dim % 16) return DUO_ERR_ARG;
+  if (r->interleaved != 0 && r->interleaved != 1) return DUO_ERR_ARG;
+  if (r->rot_dim > 0 && (!r->inv_freq || (reinterpret_cast<uintptr_t>(r->inv_freq) & 3))) return DUO_ERR_ARG;
+  if (!std::isfinite(r->mscale)) return DUO_ERR_ARG;
+  if (r->q_norm || r->k_norm) {
+    if (!std::isfinite(r->norm_eps) || r->norm_eps < 0.f) return DUO_ERR_ARG;
+    if (!aligned16(r->q_norm) || !aligned16(r->k_norm)) return DUO_ERR_ARG;
+  }
+  out->inv_freq = r->inv_freq;
+  out->q_norm = r->q_norm;
+  out->k_norm = r->k_norm;
+  out->eps = r->norm_eps;
+  out->mscale = r->mscale > 0.f ? r->mscale : 1.f;
+  out->rot_dim = r->rot_dim;
+  out->interleaved = r->interleaved;
+  return DUO_OK;
+}
+
+// A [tokens][heads][head_dim] input: 16-byte aligned rows.
+bool heads_ok(const duo_heads *h, int elt) {
+  return h && h->data && aligned16(h->data) && h->token_stride >= 0 && h->head_stride >= 0 &&
+         h->token_stride * elt % 16 == 0 && h->head_stride * elt % 16 == 0;
 }
 
 // ---------------------------------------------------------------- decode
@@ -601,10 +714,13 @@ duo_status attach_scratch(const duo_cache *c, int64_t units, int64_t slots, cons
 }
 
 // Decode attention for `rows` of a layer.  With k_new/v_new ([rows][Hkv][D])
-// each row's new token is appended in the same launch (fused step).
+// each row's new token is appended in the same launch (fused step).  With
+// check_next nothing is enqueued: the checks of a decode with one more token
+// in each row.
 duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &rows,
                        const void *q, const void *k_new, const void *v_new, void *out, float scale,
-                       const Scratch &scratch, cudaStream_t s, const Partial *part = nullptr) {
+                       const Scratch &scratch, cudaStream_t s, const Partial *part = nullptr,
+                       bool check_next = false) {
   if (!q || !std::isfinite(scale)) return DUO_ERR_ARG;
   if (part ? (!part->o || !part->lse) : !out) return DUO_ERR_ARG;
   const bool fused = k_new != nullptr;
@@ -615,8 +731,9 @@ duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
   const duo_cache_desc &d = c->desc;
   const auto &L = c->layers[layer];
   const int G = d.n_q_heads / d.n_kv_heads;
+  const int more = fused || check_next ? 1 : 0;
   for (int b : rows)
-    if (len_of(c, layer, b) + (fused ? 1 : 0) <= 0) return DUO_ERR_STATE;
+    if (len_of(c, layer, b) + more <= 0) return DUO_ERR_STATE;
   duo::DecodeConfig cfg{};
   cudaError_t e = cached_decode_config(c, &cfg);
   if (e != cudaSuccess) return launch_status(e);
@@ -661,7 +778,7 @@ duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
     int32_t rlen[duo::kMaxLaunchRows];  // retrieval keys of each row in this shard
     for (int r = 0; r < nr; ++r) {
       p.rows.row[r] = rows[g0 + r];
-      p.rows.len[r] = (int32_t)(len_of(c, layer, rows[g0 + r]) + (fused ? 1 : 0));
+      p.rows.len[r] = (int32_t)(len_of(c, layer, rows[g0 + r]) + more);
       rlen[r] = (int32_t)ret_len(c, p.rows.len[r]);
     }
     p.str_pack = plan_launch(c, layer, rlen, p.rows.len, nr, cfg, p.nsplit_r);
@@ -683,6 +800,7 @@ duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
     if (needs[i] && (st = check_scratch(c, (int64_t)nr * L.n_ret, p.cta0[nr], scratch, G)) != DUO_OK)
       return st;
   }
+  if (check_next) return DUO_OK;
   if (fused) {
     if ((st = check_room(c, layer, rows, 1)) != DUO_OK) return st;
     if ((st = reserve_blocks(c, layer, rows, 1, s)) != DUO_OK) return st;
@@ -692,7 +810,9 @@ duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
     if (needs[i] &&
         (st = attach_scratch(c, (int64_t)p.rows.n * L.n_ret, p.cta0[p.rows.n], scratch, s, &p)) != DUO_OK)
       return st;
-    if ((st = launch_status(duo::launch_decode(p, d.kv_dtype, s))) != DUO_OK) return st;
+    e = is_fp8(c) ? duo::launch_decode_fp8(duo::DecodeFp8Params{p, tail_ptrs(c, layer)}, s)
+                  : duo::launch_decode(p, d.kv_dtype, s);
+    if ((st = launch_status(e)) != DUO_OK) return st;
   }
   if (fused)
     for (int b : rows) len_of(c, layer, b) += 1;
@@ -705,8 +825,13 @@ duo_status step_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &ro
   if (!q || !out || !k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return DUO_ERR_ARG;
   const duo_cache_desc &d = c->desc;
   if (!duo::decode_can_fuse_append(d.kv_dtype, d.head_dim, d.n_q_heads / d.n_kv_heads)) {
-    // no fused kernel for this configuration: append, then attend
-    duo_status st = append_rows(c, layer, rows, k_new, v_new, 1, s);
+    // no fused kernel for this configuration: append, then attend (8-bit:
+    // the decode's checks first, so that a refused step appends nothing)
+    duo_status st = DUO_OK;
+    if (is_fp8(c) &&
+        (st = decode_rows(c, layer, rows, q, nullptr, nullptr, out, scale, scratch, s, nullptr, true)) != DUO_OK)
+      return st;
+    st = append_rows(c, layer, rows, k_new, v_new, 1, s);
     if (st != DUO_OK) return st;
     return decode_rows(c, layer, rows, q, nullptr, nullptr, out, scale, scratch, s);
   }
@@ -715,7 +840,7 @@ duo_status step_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &ro
 
 // ---------------------------------------------------------------- pre-fill
 
-// Pre-fill scratch of a 4-bit cache: the bf16 expansion of one layer's
+// Pre-fill scratch of a 4-bit or 8-bit cache: the bf16 expansion of one layer's
 // history, [retrieval K][retrieval V] at the layer's storage rows and
 // [streaming K][streaming V] as [batch][n_str][S+R][d]; the largest layer.
 struct PrefillScratch {
@@ -736,7 +861,7 @@ PrefillScratch prefill_scratch(const duo_cache *c, int layer) {
 }
 
 size_t prefill_ws_bytes(const duo_cache *c) {
-  if (c->desc.kv_dtype != DUO_INT4) return 0;
+  if (c->desc.kv_dtype != DUO_INT4 && c->desc.kv_dtype != DUO_FP8) return 0;
   int64_t m = 0;
   for (int l = 0; l < c->desc.layers; ++l) m = std::max(m, prefill_scratch(c, l).total);
   return (size_t)m;
@@ -748,23 +873,23 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
   if (!q || !k || !v || !out || C <= 0) return DUO_ERR_ARG;
   if (!std::isfinite(scale)) return DUO_ERR_ARG;
   const duo_cache_desc &d = c->desc;
-  if ((d.kv_dtype != DUO_BF16 && d.kv_dtype != DUO_INT4) || d.head_dim != 128)
+  if ((d.kv_dtype != DUO_BF16 && d.kv_dtype != DUO_INT4 && d.kv_dtype != DUO_FP8) || d.head_dim != 128)
     return DUO_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DUO_ERR_ARG;
   const auto &L = c->layers[layer];
   duo_status st = check_room(c, layer, rows, C);
   if (st != DUO_OK) return st;
   if (sharded(c)) return DUO_ERR_UNSUPPORTED;
-  const bool q4 = d.kv_dtype == DUO_INT4;
+  const bool coded = d.kv_dtype == DUO_INT4 || d.kv_dtype == DUO_FP8;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
-  if (q4) {
+  if (coded) {
     if (!ws || ws_bytes < prefill_ws_bytes(c)) return DUO_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) % kAlign) != 0) return DUO_ERR_ARG;
   }
   duo::PrefillParams p{};
   p.p = layer_ptrs(c, layer);
   duo::DequantParams dq{};
-  if (q4) {
+  if (coded) {
     // the kernel reads the bf16 expansion of the history instead of the codes
     const PrefillScratch ps = prefill_scratch(c, layer);
     dq.p = p.p;
@@ -824,9 +949,12 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
     p.k = static_cast<const uint8_t *>(k) + (int64_t)g0 * kv_row;
     p.v = static_cast<const uint8_t *>(v) + (int64_t)g0 * kv_row;
     p.out = static_cast<uint8_t *>(out) + (int64_t)g0 * q_row;
-    if (q4) {
+    if (coded) {
       dq.rows = p.rows;
-      if ((st = cuda_status(duo::launch_dequant_history(dq, s))) != DUO_OK) return st;
+      const cudaError_t e =
+          is_fp8(c) ? duo::launch_dequant_fp8(duo::DequantFp8Params{dq, tail_ptrs(c, layer)}, s)
+                    : duo::launch_dequant_history(dq, s);
+      if ((st = cuda_status(e)) != DUO_OK) return st;
     }
     if ((st = launch_status(duo::launch_prefill(p, s))) != DUO_OK) return st;
   }
@@ -906,6 +1034,68 @@ duo_status duo_append_kv_rows(duo_cache *c, int32_t layer, const int32_t *rows, 
   std::vector<int32_t> list;
   if ((st = make_rows(c, rows, n_rows, &list)) != DUO_OK) return st;
   return append_rows(c, layer, list, k, v, n_tokens, (cudaStream_t)stream);
+}
+
+duo_status duo_append_rope(duo_cache *c, int32_t layer, const duo_rope_desc *rope, const duo_heads *q,
+                           const duo_heads *k, const duo_heads *v, const int64_t *positions,
+                           int32_t n_tokens, void *q_out, duo_stream stream) {
+  return duo_append_rope_rows(c, layer, nullptr, 0, rope, q, k, v, positions, n_tokens, q_out, stream);
+}
+
+duo_status duo_append_rope_rows(duo_cache *c, int32_t layer, const int32_t *rows, int32_t n_rows,
+                                const duo_rope_desc *rope, const duo_heads *q, const duo_heads *k,
+                                const duo_heads *v, const int64_t *positions, int32_t n_tokens,
+                                void *q_out, duo_stream stream) {
+  try {
+    duo_status st = check_layer(c, layer);
+    if (st != DUO_OK) return st;
+    if (n_tokens < 0 || (q != nullptr) != (q_out != nullptr)) return DUO_ERR_ARG;
+    duo::RopeParams rp{};
+    if ((st = rope_params(rope, c->desc.head_dim, &rp)) != DUO_OK) return st;
+    std::vector<int32_t> list;
+    if ((st = make_rows(c, rows, n_rows, &list)) != DUO_OK) return st;
+    if (n_tokens > 0) {
+      const int elt = elem_bytes(c->desc.kv_dtype);
+      if (!heads_ok(k, elt) || !heads_ok(v, elt)) return DUO_ERR_ARG;
+      if (q && (!heads_ok(q, elt) || !aligned16(q_out))) return DUO_ERR_ARG;
+      if (reinterpret_cast<uintptr_t>(positions) & 7) return DUO_ERR_ARG;
+    }
+    if ((st = check_room(c, layer, list, n_tokens)) != DUO_OK) return st;
+    if (n_tokens == 0) return DUO_OK;
+    return append_rope_rows(c, layer, list, &rp, q, k, v, positions, n_tokens, q_out,
+                            (cudaStream_t)stream);
+  } catch (...) {
+    return DUO_ERR_ARG;  // out of host memory
+  }
+}
+
+duo_status duo_qk_norm_rope(const duo_rope_desc *rope, int32_t dtype, int64_t n_tokens,
+                            int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                            const duo_heads *q, const duo_heads *k, const int64_t *positions,
+                            void *q_out, void *k_out, duo_stream stream) {
+  if (dtype != DUO_F32 && dtype != DUO_BF16) return DUO_ERR_ARG;
+  if (head_dim != 64 && head_dim != 128) return DUO_ERR_ARG;
+  if (n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0 || n_q_heads + (int64_t)n_kv_heads > 65536) return DUO_ERR_ARG;
+  duo::RopeRowsParams p{};
+  duo_status st = rope_params(rope, head_dim, &p.rope);
+  if (st != DUO_OK) return st;
+  if (n_tokens == 0 || n_q_heads + n_kv_heads == 0) return DUO_OK;
+  if (n_tokens > (int64_t)1 << 40) return DUO_ERR_ARG;
+  const int elt = elem_bytes(dtype);
+  if (n_q_heads > 0 && (!heads_ok(q, elt) || !q_out || !aligned16(q_out))) return DUO_ERR_ARG;
+  if (n_kv_heads > 0 && (!heads_ok(k, elt) || !k_out || !aligned16(k_out))) return DUO_ERR_ARG;
+  if (rope->rot_dim > 0 && !positions) return DUO_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(positions) & 7) return DUO_ERR_ARG;
+  p.q = view_at(n_q_heads > 0 ? q : nullptr, 0, elt);
+  p.k = view_at(n_kv_heads > 0 ? k : nullptr, 0, elt);
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.positions = positions;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.tokens = n_tokens;
+  return launch_status(duo::launch_qk_norm_rope(p, dtype == DUO_F32 ? duo::kF32 : duo::kBF16, head_dim,
+                                                (cudaStream_t)stream));
 }
 
 duo_status duo_decode_attn(duo_cache *c, int32_t layer, const void *q, void *out, float scale,
@@ -1063,13 +1253,20 @@ duo_status duo_kv_bytes(const duo_cache *c, int64_t *kept, int64_t *full) {
   const duo_cache_desc &d = c->desc;
   const int64_t per = d.kv_dtype == DUO_INT4 ? 2 * (d.head_dim / 2 + 4)
                                              : 2 * (int64_t)d.head_dim * elem_bytes(d.kv_dtype);
+  // bytes of m tokens of a retrieval head (8-bit: full blocks coded, with
+  // their scales, the rest in bf16)
+  auto ret_bytes = [&](int64_t m) {
+    if (!is_fp8(c)) return m * per;
+    const int64_t blocks = m / duo::kScaleBlock;
+    return blocks * 2 * (duo::kScaleBlock * (int64_t)d.head_dim + 4) + m % duo::kScaleBlock * per;
+  };
   int64_t k = 0, f = 0;
   for (int l = 0; l < d.layers; ++l)
     for (int b = 0; b < d.batch; ++b) {
       const int64_t n = len_of(c, l, b);
       const int64_t win = n < c->W ? n : c->W;
-      k += (c->layers[l].n_ret * ret_len(c, n) + c->layers[l].n_str * win) * per;
-      f += (int64_t)d.n_kv_heads * n * per;
+      k += c->layers[l].n_ret * ret_bytes(ret_len(c, n)) + c->layers[l].n_str * win * per;
+      f += (int64_t)d.n_kv_heads * ret_bytes(n);
     }
   if (kept) *kept = k;
   if (full) *full = f;
@@ -1104,6 +1301,13 @@ duo_status duo_layout_info(const duo_cache *c, int32_t layer, duo_layout_view *o
   o->table_stride = c->table_stride;
   o->pool_blocks = c->pool_blocks;
   o->block_table = c->off_table;
+  return DUO_OK;
+}
+
+duo_status duo_fp8_tail_info(const duo_cache *c, int32_t layer, int64_t *tail_k, int64_t *tail_v) {
+  if (!c || layer < 0 || layer >= c->desc.layers) return DUO_ERR_ARG;
+  if (tail_k) *tail_k = c->layers[layer].off_tail_k;
+  if (tail_v) *tail_v = c->layers[layer].off_tail_v;
   return DUO_OK;
 }
 
@@ -1182,7 +1386,8 @@ duo_status duo_test_plan_decode(const duo_cache *c, int32_t layer, const int32_t
   duo::DecodeConfig cfg{};
   cfg.num_sms = num_sms;
   cfg.ctas_per_sm = ctas_per_sm;
-  cfg.tile_rows = duo::decode_mma_tile_rows(c->desc.kv_dtype == DUO_INT4 ? duo::kINT4 : duo::kBF16);
+  cfg.tile_rows = is_fp8(c) ? duo::decode_fp8_tile_rows()
+                            : duo::decode_mma_tile_rows(c->desc.kv_dtype == DUO_INT4 ? duo::kINT4 : duo::kBF16);
   int32_t len[duo::kMaxLaunchRows], rlen[duo::kMaxLaunchRows];
   int16_t ns[duo::kMaxLaunchRows];
   for (int r = 0; r < n_rows; ++r) {

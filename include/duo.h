@@ -24,7 +24,9 @@
  *  - A query at absolute position i sees key j iff j <= i and, for a streaming
  *    head, (j < S or i - j < R).  Softmax scale defaults to 1/sqrt(head_dim).
  *  - Streaming slot of position p: p if p < S, else S + ((p - S) mod R).
- *  - Q and K arrive post-RoPE; the library does no position arithmetic.
+ *  - Attention takes Q and K post-RoPE.  duo_qk_norm_rope and duo_append_rope
+ *    apply the rotation (and a per-head norm); no other call does position
+ *    arithmetic.
  *
  * Conventions:
  *  - The caller owns all device memory: the cache storage (bound once with
@@ -86,7 +88,21 @@ typedef enum duo_status {
   DUO_ERR_STATE = 8        /* cache not bound, or call out of order */
 } duo_status;
 
-typedef enum duo_kv_dtype { DUO_F32 = 0, DUO_BF16 = 1, DUO_INT4 = 2 } duo_kv_dtype;
+/* DUO_FP8 is an 8-bit cache (K/V given in bf16; head_dim 128, 1 to 8 query
+ * heads per KV head).  Retrieval heads hold e4m3 codes with one float32 scale
+ * per block of DUO_FP8_BLOCK tokens and KV head, K and V apart: the block
+ * that holds positions [32 i, 32 i + 32) of a row (of a shard, counted from
+ * its first position) has scale 2^e, the smallest e >= -120 with
+ * max|x| <= 448 * 2^e over its finite values, and code x / 2^e rounded to the
+ * nearest e4m3 (ties to even; an infinity takes the largest code, a NaN stays
+ * one).  A block is coded when it is full; until then its tokens stay in bf16
+ * in the row's tail buffer, so the cache's content depends on the tokens
+ * alone, not on how they were split into calls.  Streaming heads hold bf16
+ * rows: their ring overwrites slot by slot, which a block's scale could not
+ * follow without coding old tokens anew.  Attention reads exactly what is
+ * held: code * scale for full blocks, bf16 for the rest. */
+typedef enum duo_kv_dtype { DUO_F32 = 0, DUO_BF16 = 1, DUO_INT4 = 2, DUO_FP8 = 3 } duo_kv_dtype;
+#define DUO_FP8_BLOCK 32 /* tokens per scale of an 8-bit cache */
 
 typedef enum duo_layout {
   /* Retrieval KV heads: one contiguous [capacity, d] page each for K and V.
@@ -105,7 +121,7 @@ typedef struct duo_cache_desc {
   int32_t n_kv_heads;  /* <= DUO_MAX_KV_HEADS, divides n_q_heads */
   int32_t head_dim;    /* 64 or 128 */
   int32_t kv_dtype;    /* duo_kv_dtype */
-  int64_t capacity;    /* max tokens of one row (INT4: rounded up to 128) */
+  int64_t capacity;    /* max tokens of one row (INT4, FP8: rounded up to 128) */
 } duo_cache_desc;
 
 typedef struct duo_cache duo_cache;
@@ -117,13 +133,15 @@ typedef struct duo_layout_view {
   int32_t n_streaming;   /* streaming KV heads in this layer */
   int32_t window;        /* S + R */
   int32_t window_stride; /* rows per streaming head buffer: window, rounded up to 4 for INT4 */
-  int32_t row_bytes;     /* bytes of one token of one head: d*4 (f32), d*2 (bf16), d/2 (int4 codes) */
+  int32_t row_bytes;     /* bytes of one token of one head: d*4 (f32), d*2 (bf16), d/2 (int4 codes),
+                            d (fp8 codes; its streaming rows are d*2) */
   int64_t capacity;
   int64_t seq_len;       /* the longest row's length */
   int64_t ret_k, ret_v;  /* packed [batch][n_retrieval][capacity][row];
                             paged  [pool_blocks][n_retrieval][DUO_PAGE_TOKENS][row] */
   int64_t str_k, str_v;  /* [batch][n_streaming][window_stride][row] */
-  int64_t ret_k_sz, ret_v_sz, str_k_sz, str_v_sz; /* int4 only: fp16 (scale, zero) per token, same indexing */
+  int64_t ret_k_sz, ret_v_sz, str_k_sz, str_v_sz; /* int4: fp16 (scale, zero) per token, same indexing;
+                            fp8: ret_* float32 scale per DUO_FP8_BLOCK tokens, str_* -1 */
   int32_t kind[DUO_MAX_KV_HEADS];         /* 1 retrieval, 0 streaming, per KV head */
   int32_t packed_index[DUO_MAX_KV_HEADS]; /* index among heads of the same kind */
   int32_t layout;        /* duo_layout */
@@ -149,9 +167,9 @@ duo_status duo_cache_create(duo_cache **out, const duo_cache_desc *desc,
  * duo_cache_reset; block ids are shared by all layers of a row.
  * desc.capacity bounds one row's length.  The allocator runs on the host;
  * new block-table entries are written on the stream before the kernels that
- * need them.  Requires a configuration the tensor-core decode serves (bf16 or
- * 4-bit KV, head_dim 128); pre-fill works on both (a 4-bit cache through the
- * workspace of duo_prefill_workspace_bytes).
+ * need them.  Requires a configuration the tensor-core decode serves (bf16,
+ * 4-bit or 8-bit KV, head_dim 128); pre-fill works on each (4-bit and 8-bit
+ * caches through the workspace of duo_prefill_workspace_bytes).
  * Errors: as duo_cache_create; DUO_ERR_ARG for pool_blocks <= 0;
  * DUO_ERR_UNSUPPORTED for other configurations. */
 duo_status duo_cache_create_paged(duo_cache **out, const duo_cache_desc *desc,
@@ -203,6 +221,69 @@ duo_status duo_append_kv_rows(duo_cache *cache, int32_t layer, const int32_t *ro
                               int32_t n_rows, const void *k, const void *v,
                               int32_t n_tokens, duo_stream stream);
 
+/* A [tokens][heads][head_dim] device tensor with strides in elements, such as
+ * the queries, keys or values inside a projection's output.  Channels are
+ * contiguous; data and both strides (in bytes) are multiples of 16. */
+typedef struct duo_heads {
+  const void *data;
+  int64_t token_stride;
+  int64_t head_stride;
+} duo_heads;
+
+/* Norm and position rotation of queries and keys (the pages leave positions
+ * to the model).  A head vector x of head_dim channels becomes
+ *   y = x * rsqrt(mean(x^2) + norm_eps) * norm        (norm NULL: y = x)
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
+ *   c + i s = mscale * exp(i * position * inv_freq[j])
+ * for pair j of the first rot_dim channels: (a, b) = (j, j + rot_dim/2), or
+ * (2j, 2j + 1) when interleaved.  fp32 throughout (the angle in 64 bits, so
+ * that far positions keep their phase), rounded once to the tensors' type. */
+typedef struct duo_rope_desc {
+  int32_t rot_dim;       /* 0 (no rotation) .. head_dim, a multiple of 16 */
+  int32_t interleaved;   /* 0 or 1 */
+  const float *inv_freq; /* device [rot_dim/2]: radians per position */
+  float mscale;          /* factor of the rotation; <= 0 means 1 */
+  float norm_eps;        /* >= 0 */
+  const void *q_norm;    /* device [head_dim], the tensors' type, 16-byte aligned; or NULL */
+  const void *k_norm;    /* likewise, for keys */
+} duo_rope_desc;
+
+/* Norm and rotate the queries and keys of n_tokens tokens in one pass: q
+ * [n_tokens][n_q_heads][head_dim] and k [n_tokens][n_kv_heads][head_dim] at
+ * positions[n_tokens] (device, 64-bit; any sign) into q_out and k_out (dense).
+ * What duo_prefill_attn and duo_decode_step take.  dtype DUO_BF16 or DUO_F32,
+ * head_dim 64 or 128.  n_q_heads or n_kv_heads may be 0 (that tensor is
+ * neither read nor written).  In place (q_out == q->data with dense strides)
+ * is allowed; other overlaps are not.  positions may be NULL when rot_dim is 0.
+ * No workspace; may be captured into a graph.  Errors: DUO_ERR_ARG. */
+duo_status duo_qk_norm_rope(const duo_rope_desc *rope, int32_t dtype, int64_t n_tokens,
+                            int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                            const duo_heads *q, const duo_heads *k, const int64_t *positions,
+                            void *q_out, void *k_out, duo_stream stream);
+
+/* duo_append_kv with the keys normed and rotated on the way, and, when q is
+ * given, the same tokens' queries normed and rotated into q_out ([rows,
+ * n_tokens, n_q_heads, head_dim]): one launch (and the paged layout's table
+ * write) in place of duo_qk_norm_rope and duo_append_kv, with the same bytes
+ * in the cache (keys are rounded to the input's type before 4-bit or 8-bit
+ * coding).  Tensors have f32 (DUO_F32 caches) or bf16 elements; token i of
+ * row r is token r * n_tokens + i of k, v, q and positions.  positions (device
+ * [rows * n_tokens]) gives the rotation's positions, NULL takes each token's
+ * place in its row; where a token is stored never depends on it.  q and q_out
+ * are given together or are both NULL.  n_tokens == 0 changes nothing.
+ * Errors: as duo_append_kv, and DUO_ERR_ARG for a bad description or
+ * alignment; nothing is enqueued or changed then. */
+duo_status duo_append_rope(duo_cache *cache, int32_t layer, const duo_rope_desc *rope,
+                           const duo_heads *q, const duo_heads *k, const duo_heads *v,
+                           const int64_t *positions, int32_t n_tokens, void *q_out,
+                           duo_stream stream);
+
+/* duo_append_rope for the n_rows rows listed (rows == NULL: every row). */
+duo_status duo_append_rope_rows(duo_cache *cache, int32_t layer, const int32_t *rows,
+                                int32_t n_rows, const duo_rope_desc *rope, const duo_heads *q,
+                                const duo_heads *k, const duo_heads *v, const int64_t *positions,
+                                int32_t n_tokens, void *q_out, duo_stream stream);
+
 /* Single-token decode attention for one layer: in every row, the query at
  * position len-1 (len = that row's length) of every query head attends to its
  * KV head's visible set.  Defined by "DuoAttention: Efficient Long-Context
@@ -240,7 +321,7 @@ duo_status duo_decode_attn_rows(duo_cache *cache, int32_t layer, const int32_t *
  * launch takes the new token's K/V from the inputs (4-bit caches: quantises
  * it with duo_append_kv's encoder) and writes it to the cache; the attention
  * adds that key from the inputs.  Configurations without a fused kernel (fp32
- * caches, head_dim 64) run the two calls.  Advances each row's length
+ * and 8-bit caches, head_dim 64) run the two calls.  Advances each row's length
  * by one.  The launch uses programmatic dependent launch, so its set-up
  * overlaps the previous kernel in the stream.  Errors as for the two calls. */
 duo_status duo_decode_step(duo_cache *cache, int32_t layer, const void *q,
@@ -294,8 +375,10 @@ duo_status duo_decode_attn_static(duo_cache *cache, int32_t layer, const void *q
  * outside the Lambda band skipped.  Runs on the sm_100a tensor cores
  * (tcgen05.mma, accumulators in tensor memory, operands loaded by TMA).  Does
  * not append; call duo_append_kv with the same k/v afterwards.  Requires
- * head_dim 128 and a DUO_BF16 or DUO_INT4 cache (other cases:
+ * head_dim 128 and a DUO_BF16, DUO_INT4 or DUO_FP8 cache (other cases:
  * DUO_ERR_UNSUPPORTED).  DUO_BF16: the workspace is unused (pass NULL, 0).
+ * DUO_FP8: as DUO_INT4 below, the expansion (code * scale, or the tail's and
+ * the streaming heads' bf16 rows) being exact.
  * DUO_INT4: the part of the cache the chunk reads (retrieval keys below each
  * row's length, filled streaming slots) is first expanded to bf16, x = sc*u+zp
  * rounded to bf16, in the workspace (duo_prefill_workspace_bytes, 256-byte
@@ -304,7 +387,7 @@ duo_status duo_decode_attn_static(duo_cache *cache, int32_t layer, const void *q
  * row's length (probability 0); the expansion writes zeros there, so the
  * workspace needs no initialisation.
  * Errors: DUO_ERR_CAPACITY if len + C would pass capacity in a row;
- * DUO_ERR_WORKSPACE if an INT4 cache gets a missing or small workspace. */
+ * DUO_ERR_WORKSPACE if an INT4 or FP8 cache gets a missing or small workspace. */
 duo_status duo_prefill_attn(duo_cache *cache, int32_t layer, const void *q,
                             const void *k, const void *v, int32_t C, void *out,
                             float softmax_scale, void *workspace,
@@ -319,7 +402,7 @@ duo_status duo_prefill_attn_rows(duo_cache *cache, int32_t layer, const int32_t 
                                  size_t workspace_bytes, duo_stream stream);
 
 /* Workspace bytes duo_prefill_attn needs: 0 for a DUO_BF16 cache; for a
- * DUO_INT4 cache the bf16 size of one layer's retrieval storage rows plus its
+ * DUO_INT4 or DUO_FP8 cache the bf16 size of one layer's retrieval storage rows plus its
  * streaming buffers (K and V), for the largest layer. */
 duo_status duo_prefill_workspace_bytes(const duo_cache *cache, size_t *bytes);
 
@@ -332,7 +415,7 @@ duo_status duo_prefill_workspace_bytes(const duo_cache *cache, size_t *bytes);
  * heads), and capacity counts the rows this shard stores.  Such a cache
  * decodes only through duo_decode_attn_partial, and pre-fill is not offered.
  * Call while every length is 0 (fresh, bound or reset cache).  Tensor-core
- * decode configurations only (bf16 or 4-bit KV, head_dim 128).
+ * decode configurations only (bf16, 4-bit or 8-bit KV, head_dim 128).
  * Errors: DUO_ERR_ARG (lo < 0 or hi <= lo), DUO_ERR_STATE (tokens present),
  * DUO_ERR_UNSUPPORTED (other configurations). */
 duo_status duo_set_retrieval_shard(duo_cache *cache, int64_t lo, int64_t hi);
@@ -381,19 +464,27 @@ duo_status duo_pool_free_blocks(const duo_cache *cache, int64_t *free_blocks);
 /* KV bytes held now (kept) and what a full cache of every head would hold
  * (full_equivalent): kept = sum over layers, rows, KV heads of
  * (retrieval ? n : min(n, S+R)) * bytes_per_token_per_head, n = the row's
- * length in that layer. */
+ * length in that layer (8-bit retrieval heads: codes and scales of the full
+ * blocks, bf16 for the tokens past them). */
 duo_status duo_kv_bytes(const duo_cache *cache, int64_t *kept,
                         int64_t *full_equivalent);
 
 duo_status duo_layout_info(const duo_cache *cache, int32_t layer,
                            duo_layout_view *out);
 
+/* DUO_FP8: byte offsets of the layer's tail buffers, bf16 [batch][n_retrieval]
+ * [DUO_FP8_BLOCK][head_dim] each for K and V (row slot j holds the j-th token
+ * past the row's last full block); -1 for other types or without retrieval
+ * heads.  Either pointer may be NULL. */
+duo_status duo_fp8_tail_info(const duo_cache *cache, int32_t layer, int64_t *tail_k,
+                             int64_t *tail_v);
+
 /* Force the split count of retrieval decode (1..DUO_MAX_SPLITS), or 0 for the
  * automatic choice (enough splits to fill every SM once).  The result never
  * depends on it beyond rounding. */
 duo_status duo_set_decode_splits(duo_cache *cache, int32_t splits);
 
-/* How the tensor-core decode (bf16 and 4-bit caches, head_dim 128) shares a
+/* How the tensor-core decode (bf16, 4-bit and 8-bit caches, head_dim 128) shares a
  * split retrieval head's keys among its splits.  By default (on = 0) each
  * split takes a fixed share of 13/16 of the key tiles (7/8 on a 4-bit cache)
  * and the rest goes, one tile at a time, to whichever warps finish first, so
@@ -408,7 +499,7 @@ duo_status duo_set_decode_splits(duo_cache *cache, int32_t splits);
 duo_status duo_set_decode_reproducible(duo_cache *cache, int32_t on);
 
 /* Element type of decode outputs: DUO_BF16 (the default for DUO_BF16 and
- * DUO_INT4 caches) or DUO_F32 (float32; the only type of a DUO_F32 cache).
+ * DUO_INT4 and DUO_FP8 caches) or DUO_F32 (float32; the only type of a DUO_F32 cache).
  * Applies to duo_decode_attn, duo_decode_step, duo_decode_attn_static and
  * their *_rows forms: out is then [rows, n_q_heads, head_dim] of that type.
  * The kernels accumulate in float32 either way; DUO_F32 skips the final
@@ -424,7 +515,7 @@ duo_status duo_decode_splits(const duo_cache *cache, int32_t layer,
 
 /* Streaming heads per streaming CTA that the next decode of this layer will
  * use (a scheduling choice; the pages have no counterpart).  The tensor-core
- * decode (bf16 and 4-bit caches) may run 2, 4 or 8 of a row's streaming heads
+ * decode (bf16, 4-bit and 8-bit caches) may run 2, 4 or 8 of a row's streaming heads
  * in one CTA, one group of warps each, when their windows are short next to the
  * retrieval splits: the SMs this frees take more retrieval splits.  1 for
  * every other configuration.  Outputs do not depend on it beyond rounding.

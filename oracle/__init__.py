@@ -15,11 +15,13 @@ cache      the scalar ring-buffer append/evict simulation and the expected
            cache contents, plus the kept-KV byte count for a head mask
 int4       the fp32 mirror of the asymmetric 4-bit KV quantiser and its
            exact dequantisation
+fp8        the blocks of the 8-bit cache: scales, e4m3 codes, held values
+rotary     per-head RMS norm and position rotation
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
-(``tests/test_oracle_pins.py``); none is "parity unpinned" except the pages'
+(``tests/test_oracle_pins.py``, ``tests/test_fp8_rotary_cpu.py``); none is "parity unpinned" except the pages'
 own memory-reduction figures, which the byte formula does not reproduce (the
 pages never state the basis of their ratio).
 """
 
-from . import attention, cache, int4  # noqa: F401
+from . import attention, cache, fp8, int4, rotary  # noqa: F401
