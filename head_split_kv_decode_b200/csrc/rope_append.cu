@@ -14,166 +14,114 @@
 // DuoAttention" (what each kind of head keeps); the pages leave positions to
 // the model.
 //
-// A warp takes one token and a group of its head vectors: the angles and
-// their sines depend on the token only, so they are computed once per group
-// and reused for every head.  CPL channels per lane; the partner of a rotated
-// channel is in the same lane (interleaved pairs) or CPL-aligned in another
-// lane of the same vector, one shuffle per channel.
+// Layout.  A vector's channels are spread over D/8 lanes, 8 each: two quads of
+// 4, chosen so that both channels of every rotated pair are in one lane
+// (quads i and i + rot_dim/8, or neighbours when interleaved), so rotating
+// needs no exchange.  Row CTAs take kTok tokens: the tokens' sines and cosines
+// go to shared memory once (one angle per thread) and serve all their
+// vectors, each lane holding the four (cos, sin) of its pairs.
 //
-// 8-bit cache: a CTA takes one scale block (32 tokens) of one or more
-// retrieval heads.  A block that the call completes is coded as a whole, its
-// older tokens read from the bf16 tail; tokens of a block that stays open go
-// to the tail.  scale = 2^e, the smallest e >= -120 with max|x| <= 448 * 2^e
-// (finite values), code = x / scale rounded to nearest even e4m3, saturating
-// (an infinity takes the largest code, a NaN stays one).  A power of two makes
-// the division and the expansion to bf16 exact.
+// 8-bit cache: a CTA takes the K or V of one scale block (32 tokens) of one or
+// more retrieval heads.  A block that the call completes is coded as a whole,
+// its older tokens read from the bf16 tail; tokens of a block that stays open
+// go to the tail.  scale = 2^e, the smallest e >= -120 with max|x| <= 448 *
+// 2^e (finite values), code = x / scale rounded to nearest even e4m3,
+// saturating (an infinity takes the largest code, a NaN stays one).  A power
+// of two makes the division and the expansion to bf16 exact.
 #include <algorithm>
 
 #include "common.cuh"
 #include "kv8.h"
-#include "quant_int4.cuh"
 
 namespace duo {
 namespace ra {
 
 enum Mode : int { kAlone = 0, kRaw = 1, kInt4 = 2, kFp8Mode = 3 };
 
-template <typename T, int CPL>
-struct Lane {  // CPL channels of one lane, as fp32
-  __device__ __forceinline__ static void load(const T *p, float (&x)[CPL]) {
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (CPL >= 4) {
-#pragma unroll
-        for (int i = 0; i < CPL / 4; ++i) {
-          const float4 v = reinterpret_cast<const float4 *>(p)[i];
-          x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) x[i] = p[i];
-      }
-    } else {
-      uint32_t w[CPL / 2];
-      if constexpr (CPL == 8) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      } else if constexpr (CPL == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-      }
-#pragma unroll
-      for (int i = 0; i < CPL / 2; ++i) {
-        const float2 f = bf16x2_to_f2(w[i]);
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
-      }
-    }
-  }
-  __device__ __forceinline__ static void store(T *p, const float (&x)[CPL]) {
-    if constexpr (sizeof(T) == 4) {
-      if constexpr (CPL >= 4) {
-#pragma unroll
-        for (int i = 0; i < CPL / 4; ++i)
-          reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) p[i] = x[i];
-      }
-    } else {
-      uint32_t w[CPL / 2];
-#pragma unroll
-      for (int i = 0; i < CPL / 2; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-      if constexpr (CPL == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      else if constexpr (CPL == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t *>(p) = w[0];
-    }
-  }
+constexpr int kThreads = 256;
+constexpr int kTok = 4;     // tokens of a row CTA
+constexpr int kBatch = 4;   // vectors a lane group loads at once
+
+// Four channels of one lane.
+__device__ __forceinline__ void load_quad(const float *p, float *x) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_quad(const __nv_bfloat16 *p, float *x) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = bf16x2_to_f2(v.x), b = bf16x2_to_f2(v.y);
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+__device__ __forceinline__ void store_quad(float *p, const float *x) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_quad(__nv_bfloat16 *p, const float *x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2 *>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// First channels of a lane's two quads.
+struct Quads {
+  int a, b;
 };
+__device__ __forceinline__ Quads quads_of(const RopeParams &r, int sl) {
+  const int n = r.interleaved ? 0 : r.rot_dim >> 3;  // lanes whose quads are partners
+  if (sl < n) return {4 * sl, 4 * (sl + n)};
+  return {8 * sl, 8 * sl + 4};
+}
 
-// cos and sin (times mscale) of this lane's channels at one position.  sn
-// carries the sign of the channel's own side of its pair: out = x * cs +
-// partner * sn.  Channels past rot_dim get (1, 0).
-template <typename T, int CPL>
-__device__ __forceinline__ void rotation(const RopeParams &r, int64_t pos, int c0, float (&cs)[CPL],
-                                         float (&sn)[CPL]) {
-  constexpr double kPerTurn = 0.15915494309189533576888;  // 1 / (2 pi)
-  const int half = r.rot_dim >> 1;
-  const double p = (double)pos * kPerTurn;
-#pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int c = c0 + j;
-    if (c >= r.rot_dim) {
-      cs[j] = 1.f;
-      sn[j] = 0.f;
-      continue;
-    }
-    const int pair = r.interleaved ? c >> 1 : (c < half ? c : c - half);
-    const double turns = p * (double)r.inv_freq[pair];
-    const float f = (float)(turns - rint(turns));  // [-1/2, 1/2]
-    float s, k;
-    if constexpr (sizeof(T) == 4) {
-      sincospif(2.f * f, &s, &k);
-    } else {
-      // the hardware's sine and cosine are off by about 2^-21 on [-pi, pi],
-      // far below the half step 2^-8 of the bf16 result
-      __sincosf(6.283185307179586f * f, &s, &k);
-    }
-    const bool second = r.interleaved ? (c & 1) : (c >= half);
-    cs[j] = k * r.mscale;
-    sn[j] = (second ? s : -s) * r.mscale;
+// mscale * (cos, sin) of pair `pair` at position pos.
+__device__ __forceinline__ float2 angle(const RopeParams &r, double pos_turns, int pair) {
+  const double turns = pos_turns * (double)r.inv_freq[pair];
+  float s, c;
+  sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+  return make_float2(c * r.mscale, s * r.mscale);
+}
+constexpr double kPerTurn = 0.15915494309189533576888;  // 1 / (2 pi)
+
+// Sines and cosines of NT tokens into shared memory, [token][D/2] each; pairs
+// past rot_dim/2 turn by nothing.  pos(i) gives token i's position.
+template <int D, int NT, typename PosFn>
+__device__ __forceinline__ void fill_angles(const RopeParams &r, float *s_cos, float *s_sin, PosFn pos) {
+  for (int i = threadIdx.x; i < NT * (D / 2); i += kThreads) {
+    const int pair = i % (D / 2);
+    float2 cs = make_float2(1.f, 0.f);
+    if (pair < (r.rot_dim >> 1)) cs = angle(r, (double)pos(i / (D / 2)) * kPerTurn, pair);
+    s_cos[i] = cs.x;
+    s_sin[i] = cs.y;
   }
 }
 
-// Sum of squares over a vector: one tree over its channel pairs, in the same
-// order whatever the lanes hold, so that every kernel here gives the same bits.
-template <int LPR, int CPL>
-__device__ __forceinline__ float sum_squares(const float (&x)[CPL]) {
-  float s[CPL / 2];
+// Sum over the LPR lanes of a vector.
+template <int LPR>
+__device__ __forceinline__ float vec_sum(float v) {
 #pragma unroll
-  for (int i = 0; i < CPL / 2; ++i) s[i] = fmaf(x[2 * i + 1], x[2 * i + 1], x[2 * i] * x[2 * i]);
-#pragma unroll
-  for (int n = CPL / 4; n > 0; n >>= 1)
-#pragma unroll
-    for (int i = 0; i < n; ++i) s[i] = s[2 * i] + s[2 * i + 1];
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
-  return s[0];
+  for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-// Norm (w non-null) and rotation of one vector; every lane of the warp calls.
-template <typename T, int D, int CPL>
-__device__ __forceinline__ void norm_rotate(const RopeParams &r, const void *w, int sl,
-                                            const float (&cs)[CPL], const float (&sn)[CPL],
-                                            float (&x)[CPL]) {
-  constexpr int LPR = D / CPL;
-  if (w) {
-    const float inv = rsqrtf(sum_squares<LPR, CPL>(x) * (1.f / D) + r.eps);
-    float wv[CPL];
-    Lane<T, CPL>::load(static_cast<const T *>(w) + sl * CPL, wv);
+// Norm of one vector with the lane's weights w.
+template <int D>
+__device__ __forceinline__ void norm8(float eps, const float (&w)[8], float (&x)[8]) {
+  float s[4];
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) x[j] = x[j] * inv * wv[j];
-  }
-  if (r.rot_dim == 0) return;
-  if (r.interleaved) {
+  for (int i = 0; i < 4; ++i) s[i] = fmaf(x[2 * i + 1], x[2 * i + 1], x[2 * i] * x[2 * i]);
+  const float ss = vec_sum<D / 8>((s[0] + s[1]) + (s[2] + s[3]));
+  const float inv = rsqrtf(ss * (1.f / D) + eps);
 #pragma unroll
-    for (int j = 0; j < CPL; j += 2) {
-      const float a = x[j], b = x[j + 1];
-      x[j] = fmaf(a, cs[j], b * sn[j]);
-      x[j + 1] = fmaf(b, cs[j + 1], a * sn[j + 1]);
-    }
-  } else {
-    // the partner channels are half / CPL lanes further (first half) or back
-    const int lanes = (r.rot_dim >> 1) / CPL;
-    const int from = (threadIdx.x & 31) + (sl < lanes ? lanes : (sl < 2 * lanes ? -lanes : 0));
+  for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * w[j];
+}
+
+// Rotation of the lane's four pairs.
+__device__ __forceinline__ void rotate8(bool interleaved, const float4 &c, const float4 &s, float (&x)[8]) {
+  const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      const float partner = __shfl_sync(0xffffffffu, x[j], from);
-      x[j] = fmaf(x[j], cs[j], partner * sn[j]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float a = interleaved ? x[2 * i] : x[i], b = interleaved ? x[2 * i + 1] : x[4 + i];
+    const float na = fmaf(a, cc[i], -(b * sn[i])), nb = fmaf(b, cc[i], a * sn[i]);
+    if (interleaved) x[2 * i] = na, x[2 * i + 1] = nb;
+    else x[i] = na, x[4 + i] = nb;
   }
 }
 
@@ -189,10 +137,12 @@ __device__ __forceinline__ int scale_exp(float amax) {
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
+// Four codes of x * inv, first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(const float *x, float inv) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
+  return lo | (uint32_t)hi << 16;
 }
 
 __device__ __forceinline__ float finite_abs(float x) {
@@ -200,16 +150,13 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;  // infinities and NaN do not set the scale
 }
 
-constexpr int kThreads = 256;
-
-// One scale-block CTA: launch row r, heads [h0, h1), item `item` (see the
-// launch).  256 threads = 16 half-warps of 16 lanes, 2 tokens each.
-template <int D>
-__device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, int h0, int h1, int item) {
-  static_assert(D == 128, "the 8-bit cache has head_dim 128");
+// One scale-block CTA: launch row r, K or V (isv), heads [h0, h1), item `item`
+// (see the launch).  256 threads = 16 half-warps, 2 tokens each.
+__device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool isv, int h0, int h1,
+                                          int item, float *s_cos, float *s_sin) {
   using bf = __nv_bfloat16;
-  constexpr int CPL = 8;
-  __shared__ float s_max[2][2][kThreads / 32];
+  constexpr int D = 128;
+  __shared__ float s_max[2][kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5;
   const int hw = tid >> 4, sl = tid & 15;  // half-warp, lane in the vector
   const AppendParams &a = P.a;
@@ -222,8 +169,19 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, int h0
   if (l1 <= l0) return;
   const int64_t fb = l0 >> kScaleShift, done = l1 >> kScaleShift;  // blocks [fb, done) become full
   const bool open = (l1 & (kScaleBlock - 1)) != 0;
-  const int n_items = (int)max((int64_t)1, done - fb);
-  if (item >= n_items) return;
+  if (item >= (int)max((int64_t)1, done - fb)) return;
+  const bool turn = !isv && P.rope.rot_dim > 0;
+  const bool norm = !isv && P.rope.k_norm != nullptr;
+  const Quads qd = quads_of(P.rope, sl);
+  float w[8];
+  if (norm) {
+    load_quad(static_cast<const bf *>(P.rope.k_norm) + qd.a, w);
+    load_quad(static_cast<const bf *>(P.rope.k_norm) + qd.b, w + 4);
+  }
+  const HeadView &in = isv ? P.v : P.k;
+  bf *tails = reinterpret_cast<bf *>(isv ? P.tail.v : P.tail.k);
+  uint8_t *codes = isv ? a.p.ret_v : a.p.ret_k;
+  float *scales = reinterpret_cast<float *>(isv ? a.p.ret_v_sz : a.p.ret_k_sz);
   int buf = 0;
   // Item 0 also writes the block that stays open, after the first block's
   // older tokens have been read from the same tail rows.
@@ -232,245 +190,291 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, int h0
     const bool full = part == 0;
     if (part == 0 && blk >= done) continue;
     if (part == 1 && (item != 0 || !open)) break;
-    if (part == 1) __syncthreads();
-    float cs[2][CPL] = {}, sn[2][CPL] = {};
-    const bf *src_k[2], *src_v[2];
+    const int64_t first = blk << kScaleShift;  // local row of the block's first token
+    const int64_t t0 = first + a.shard_lo - len;  // its token of the call (negative: older)
+    const int64_t tok0 = (int64_t)r * a.n_tok + t0;
+    const bf *src[2];
     bool fresh[2], have[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t l = (blk << kScaleShift) + hw * 2 + i;  // local row
+      const int64_t l = first + hw * 2 + i;
       fresh[i] = l >= l0 && l < l1;
       have[i] = full || fresh[i];
-      const int64_t t = l + a.shard_lo - len;               // token of the call
-      const int64_t tok = (int64_t)r * a.n_tok + t;
-      src_k[i] = static_cast<const bf *>(P.k.p) + tok * P.k.tok;
-      src_v[i] = static_cast<const bf *>(P.v.p) + tok * P.v.tok;
-      if (fresh[i] && P.rope.rot_dim)
-        rotation<bf, CPL>(P.rope, P.positions ? P.positions[tok] : len + t, sl * CPL, cs[i], sn[i]);
+      src[i] = static_cast<const bf *>(in.p) + (tok0 + hw * 2 + i) * in.tok;
     }
-    for (int h = h0; h < h1; ++h) {
+    // a head's two vectors of this half-warp; the next head's are loaded
+    // before this one's are exchanged
+    auto fetch = [&](int h, float (&x)[2][8]) {
       const int kvh = a.h.ret_heads[h];
-      bf *tk = reinterpret_cast<bf *>(P.tail.k) + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
-      bf *tv = reinterpret_cast<bf *>(P.tail.v) + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
-      float k[2][CPL], v[2][CPL];
+      const bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int slot = hw * 2 + i;
-        const bf *pk = fresh[i] ? src_k[i] + (int64_t)kvh * P.k.head : tk + slot * D;
-        const bf *pv = fresh[i] ? src_v[i] + (int64_t)kvh * P.v.head : tv + slot * D;
+        const bf *p = fresh[i] ? src[i] + (int64_t)kvh * in.head : tail + (hw * 2 + i) * D;
         if (have[i]) {
-          Lane<bf, CPL>::load(pk + sl * CPL, k[i]);
-          Lane<bf, CPL>::load(pv + sl * CPL, v[i]);
+          load_quad(p + qd.a, x[i]);
+          load_quad(p + qd.b, x[i] + 4);
         } else {
 #pragma unroll
-          for (int j = 0; j < CPL; ++j) k[i][j] = v[i][j] = 0.f;
+          for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
         }
       }
-      float mk = 0.f, mv = 0.f;
+    };
+    float x[2][8];
+    fetch(h0, x);
+    if (part == 1) __syncthreads();  // angles and tail of part 0 are no longer read
+    if (turn)
+      fill_angles<D, kScaleBlock>(P.rope, s_cos, s_sin, [&](int i) {
+        const int64_t t = t0 + i;
+        // older tokens (and those past the call's) are not rotated
+        if (t < 0 || t >= a.n_tok) return (int64_t)0;
+        return P.positions ? P.positions[tok0 + i] : len + t;
+      });
+    __syncthreads();
+    for (int h = h0; h < h1; ++h) {
+      float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // the two vectors of a warp's halves may differ in kind (tail or
-        // new): all lanes rotate, the tail's keep what they had
-        float x[CPL];
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) x[j] = k[i][j];
-        norm_rotate<bf, D, CPL>(P.rope, P.rope.k_norm, sl, cs[i], sn[i], x);
+        for (int j = 0; j < 8; ++j) y[j] = x[i][j];
+        if (norm) norm8<D>(P.rope.eps, w, y);
+        if (turn) {
+          const int at = (hw * 2 + i) * (D / 2) + 4 * sl;
+          const float4 c = *reinterpret_cast<const float4 *>(s_cos + at);
+          const float4 s = *reinterpret_cast<const float4 *>(s_sin + at);
+          if (P.rope.interleaved) rotate8(true, c, s, y);
+          else rotate8(false, c, s, y);
+        }
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
+        for (int j = 0; j < 8; ++j) {
           // rounded to bf16 first: what the rotated keys are everywhere else
-          if (fresh[i]) k[i][j] = __bfloat162float(__float2bfloat16_rn(x[j]));
-          mk = fmaxf(mk, finite_abs(k[i][j]));
-          mv = fmaxf(mv, finite_abs(v[i][j]));
+          if (fresh[i]) x[i][j] = __bfloat162float(__float2bfloat16_rn(y[j]));
+          mx = fmaxf(mx, finite_abs(x[i][j]));
         }
       }
+      float z[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] = x[i][j];
+      if (h + 1 < h1) fetch(h + 1, x);
       if (!full) {
+        bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!fresh[i]) continue;
-          const int slot = hw * 2 + i;
-          Lane<bf, CPL>::store(tk + slot * D + sl * CPL, k[i]);
-          Lane<bf, CPL>::store(tv + slot * D + sl * CPL, v[i]);
+          store_quad(tail + (hw * 2 + i) * D + qd.a, z[i]);
+          store_quad(tail + (hw * 2 + i) * D + qd.b, z[i] + 4);
         }
         continue;
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-      }
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // two sets of slots in turn: one barrier a head
-      if ((tid & 31) == 0) {
-        s_max[buf][0][warp] = mk;
-        s_max[buf][1][warp] = mv;
-      }
+      if ((tid & 31) == 0) s_max[buf][warp] = mx;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) {
-        mk = fmaxf(mk, s_max[buf][0][i]);
-        mv = fmaxf(mv, s_max[buf][1][i]);
-      }
+      for (int i = 0; i < kThreads / 32; ++i) mx = fmaxf(mx, s_max[buf][i]);
       buf ^= 1;
-      const int ek = scale_exp(mk), ev = scale_exp(mv);
-      const float ik = pow2i(-ek), iv = pow2i(-ev);
-      const int64_t row = ret_row(a.ret, b, h, blk << kScaleShift);
+      const int e = scale_exp(mx);
+      const float inv = pow2i(-e);
+      const int64_t row = ret_row(a.ret, b, h, first);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint16_t ck[CPL / 2], cv[CPL / 2];
-#pragma unroll
-        for (int j = 0; j < CPL / 2; ++j) {
-          ck[j] = e4m3x2(k[i][2 * j] * ik, k[i][2 * j + 1] * ik);
-          cv[j] = e4m3x2(v[i][2 * j] * iv, v[i][2 * j + 1] * iv);
-        }
-        const int64_t at = (row + hw * 2 + i) * D + sl * CPL;
-        *reinterpret_cast<uint2 *>(a.p.ret_k + at) =
-            make_uint2(ck[0] | (uint32_t)ck[1] << 16, ck[2] | (uint32_t)ck[3] << 16);
-        *reinterpret_cast<uint2 *>(a.p.ret_v + at) =
-            make_uint2(cv[0] | (uint32_t)cv[1] << 16, cv[2] | (uint32_t)cv[3] << 16);
+        uint8_t *at = codes + (row + hw * 2 + i) * D;
+        *reinterpret_cast<uint32_t *>(at + qd.a) = e4m3x4(z[i], inv);
+        *reinterpret_cast<uint32_t *>(at + qd.b) = e4m3x4(z[i] + 4, inv);
       }
-      if (tid == 0) {
-        reinterpret_cast<float *>(a.p.ret_k_sz)[row >> kScaleShift] = pow2i(ek);
-        reinterpret_cast<float *>(a.p.ret_v_sz)[row >> kScaleShift] = pow2i(ev);
-      }
+      if (tid == 0) scales[row >> kScaleShift] = pow2i(e);
     }
   }
 }
 
 // ------------------------------------------------------------ vectors
 
-// Work of the row CTAs: (token, group of RPW * NIT head vectors) per warp.
-// Head vectors of a token: the Hq queries (when given), then the K heads and,
-// for an append, the V heads; 8-bit caches list their streaming heads only.
-template <typename T, int D, int MODE, int NIT>
+// 4-bit codes of a vector, this lane's quads (a, b): the arithmetic of the
+// 4-bit append (quant_int4.cuh), the extremes over D/8 lanes.
+template <int D>
+__device__ __forceinline__ void quantise8(const float (&x)[8], uint32_t *qa, uint32_t *qb, __half2 *sz) {
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    mn = fminf(mn, x[j]);
+    mx = fmaxf(mx, x[j]);
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const __half sch = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
+  const __half zph = __float2half_rn(mn);
+  const float scf = __half2float(sch), zpf = __half2float(zph);
+  uint32_t u[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float q = 0.0f;
+    if (scf != 0.0f) q = fminf(15.0f, fmaxf(0.0f, rintf(__fdiv_rn(__fsub_rn(x[j], zpf), scf))));
+    u[j >> 2] |= (uint32_t)q << (4 * (j & 3));
+  }
+  *qa = u[0];
+  *qb = u[1];
+  sz->x = sch;
+  sz->y = zph;
+}
+
+// Row CTAs: kTok tokens x vecs_per_cta of their head vectors: the Hq queries
+// (when given), then the K heads and, for an append, the V heads; 8-bit
+// caches list their streaming heads only.  A group of D/8 lanes keeps to one
+// token.
+template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_constant__ RopeRowsParams P,
-                                                             int block_ctas) {
-  // 4-bit codes are made by a whole warp per vector (quantize_row_int4)
-  constexpr int CPL = MODE == kInt4 ? D / 32 : 8;
-  constexpr int LPR = D / CPL, RPW = 32 / LPR;
+                                                             int block_ctas, int vecs_per_cta) {
+  constexpr int LPR = D / 8, GROUPS = kThreads / LPR, SUB = GROUPS / kTok;
+  // the 8-bit mode's scale-block CTAs hold 32 tokens' angles
+  constexpr int NT = MODE == kFp8Mode ? kScaleBlock : kTok;
+  __shared__ __align__(16) float s_cos[NT * (D / 2)], s_sin[NT * (D / 2)];
   const AppendParams &a = P.a;
   if constexpr (MODE == kFp8Mode) {
     if ((int)blockIdx.x < block_ctas) {
       const int groups = (a.n_ret + P.heads_per_cta - 1) / P.heads_per_cta;
-      const int item = blockIdx.x % P.block_items;
-      const int y = blockIdx.x / P.block_items;
+      int y = blockIdx.x;
+      const bool isv = y & 1;
+      y >>= 1;
+      const int item = y % P.block_items;
+      y /= P.block_items;
       const int h0 = (y % groups) * P.heads_per_cta;
-      block_cta<D>(P, y / groups, h0, min(a.n_ret, h0 + P.heads_per_cta), item);
+      block_cta(P, y / groups, isv, h0, min(a.n_ret, h0 + P.heads_per_cta), item, s_cos, s_sin);
       return;
     }
   }
-  const int lane = threadIdx.x & 31, sl = lane % LPR, sub = lane / LPR;
   const int nq = P.q.p ? P.Hq : 0;
   const int nk = MODE == kFp8Mode ? a.n_str : P.Hkv;
   const int vecs = nq + (MODE == kAlone ? nk : 2 * nk);
-  if (vecs == 0) return;
-  const int groups = (vecs + RPW * NIT - 1) / (RPW * NIT);
-  const int64_t warps = P.tokens * groups;
-  const int64_t stride = (int64_t)(gridDim.x - block_ctas) * (kThreads / 32);
-  for (int64_t w = (int64_t)(blockIdx.x - block_ctas) * (kThreads / 32) + (threadIdx.x >> 5); w < warps;
-       w += stride) {
-    const int64_t tok = w / groups;
-    const int v0 = (int)(w % groups) * RPW * NIT;
-    // where the token goes in the cache
-    int lr = 0, b = 0;
-    int64_t p = 0, end = 0;
-    if constexpr (MODE != kAlone) {
-      lr = (int)(tok / a.n_tok);
-      b = a.rows.row[lr];
-      p = a.rows.len[lr] + (tok - lr * a.n_tok);
-      end = a.rows.len[lr] + a.n_tok;
+  const int vgroups = (vecs + vecs_per_cta - 1) / vecs_per_cta;
+  const int64_t cta = (int64_t)blockIdx.x - block_ctas;
+  const int v0 = (int)(cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
+  const int64_t tok0 = cta / vgroups * kTok;
+  const int group = threadIdx.x / LPR, sl = threadIdx.x % LPR;
+  const int64_t tok = tok0 + group % kTok;
+  const bool alive = tok < P.tokens;
+  const Quads qd = quads_of(P.rope, sl);
+  // where the token goes in the cache: rows of its heads, one stride apart
+  int64_t p = 0, ret0 = 0, ret_step = 0, str0 = 0;
+  bool kept_ret = true, kept_str = true;
+  if constexpr (MODE != kAlone) {
+    if (alive) {
+      const int lr = (int)(tok / a.n_tok);
+      const int b = a.rows.row[lr];
+      const int64_t len = a.rows.len[lr];
+      p = len + (tok - lr * a.n_tok);
+      kept_ret = p >= a.shard_lo && p < a.shard_hi;
+      kept_str = p < a.S || p >= len + a.n_tok - a.R;
+      if (MODE != kFp8Mode && a.n_ret > 0 && kept_ret) {
+        ret0 = ret_row(a.ret, b, 0, p - a.shard_lo);
+        ret_step = a.ret.table ? kPageTokens : a.ret.cap;
+      }
+      if (kept_str) str0 = (int64_t)b * a.n_str * a.Ws + ring_slot(p, a.S, a.R);
     }
-    const bool kept_ret = MODE == kAlone || (p >= a.shard_lo && p < a.shard_hi);
-    const bool kept_str = MODE == kAlone || p < a.S || p >= end - a.R;
-    float x[NIT][CPL];
-    int vec[NIT];   // this lane's vector, -1: none
+  }
+  if constexpr (MODE != kAlone) {
+    // nothing of these tokens is kept (a long chunk's middle, streaming heads)
+    const bool any = alive && ((MODE != kFp8Mode && a.n_ret > 0 && kept_ret) || (a.n_str > 0 && kept_str));
+    if (v0 >= nq && !__syncthreads_or(any)) return;
+  }
+  // the first batch's loads are on their way while the angles are formed
+  float x[kBatch][8];
+  int vec[kBatch];  // this group's vector, -1: none
+  auto fetch = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < NIT; ++i) {
-      int vi = v0 + i * RPW + sub;
+    for (int i = 0; i < kBatch; ++i) {
+      const int vi = base + i * SUB;
       const T *src = nullptr;
-      if (vi < nq) {
-        src = static_cast<const T *>(P.q.p) + tok * P.q.tok + (int64_t)vi * P.q.head;
-      } else if (vi < vecs) {
-        const bool isv = vi >= nq + nk;
-        const int h = vi - nq - (isv ? nk : 0);
-        const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
-        const HeadView &in = isv ? P.v : P.k;
-        if (MODE == kAlone || (a.h.kind[kvh] ? kept_ret : kept_str))
-          src = static_cast<const T *>(in.p) + tok * in.tok + (int64_t)kvh * in.head;
-      }
-      if (src) {
-        Lane<T, CPL>::load(src + sl * CPL, x[i]);
-      } else {
-        vi = -1;
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) x[i][j] = 0.f;
-      }
-      vec[i] = vi;
-    }
-    float cs[CPL], sn[CPL];
-    if (P.rope.rot_dim && v0 < nq + nk)
-      rotation<T, CPL>(P.rope, P.positions ? P.positions[tok] : p, sl * CPL, cs, sn);
-#pragma unroll
-    for (int i = 0; i < NIT; ++i) {
-      // queries and keys; a warp may hold both and values too, so the norm's
-      // weight is chosen per half and values keep what was loaded
-      const int base = v0 + i * RPW;  // the warp's first vector of this step
-      if (base < nq + nk) {
-        float y[CPL];
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) y[j] = x[i][j];
-        const int vi = base + sub;
-        const void *wq = P.rope.q_norm, *wk = P.rope.k_norm;
-        const bool mixed = base < nq && base + RPW > nq;
-        const void *w = vi < nq ? wq : wk;
-        if (!mixed || (wq != nullptr) == (wk != nullptr)) {
-          norm_rotate<T, D, CPL>(P.rope, w, sl, cs, sn, y);
+      if (alive && vi < v1) {
+        if (vi < nq) {
+          src = static_cast<const T *>(P.q.p) + tok * P.q.tok + (int64_t)vi * P.q.head;
         } else {
-          // only one of the two is normed: the other half's result is replaced
-          float z[CPL];
-#pragma unroll
-          for (int j = 0; j < CPL; ++j) z[j] = y[j];
-          norm_rotate<T, D, CPL>(P.rope, wq ? wq : wk, sl, cs, sn, y);
-          norm_rotate<T, D, CPL>(P.rope, nullptr, sl, cs, sn, z);
-#pragma unroll
-          for (int j = 0; j < CPL; ++j) y[j] = w ? y[j] : z[j];
+          const bool isv = vi >= nq + nk;
+          const int h = vi - nq - (isv ? nk : 0);
+          const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
+          const HeadView &in = isv ? P.v : P.k;
+          if (MODE == kAlone || (a.h.kind[kvh] ? kept_ret : kept_str))
+            src = static_cast<const T *>(in.p) + tok * in.tok + (int64_t)kvh * in.head;
         }
-        if (vi < nq + nk) {
+      }
+      vec[i] = src ? vi : -1;
+      if (src) {
+        load_quad(src + qd.a, x[i]);
+        load_quad(src + qd.b, x[i] + 4);
+      } else {
 #pragma unroll
-          for (int j = 0; j < CPL; ++j) x[i][j] = y[j];
-        }
+        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+      }
+    }
+  };
+  const int sub = group / kTok;
+  fetch(v0 + sub);
+  const bool turn = P.rope.rot_dim > 0 && v0 < nq + nk;
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (turn) {
+    fill_angles<D, kTok>(P.rope, s_cos, s_sin, [&](int i) {
+      const int64_t tk = min(tok0 + i, P.tokens - 1);
+      if (MODE == kAlone || P.positions) return P.positions[tk];
+      const int lr = (int)(tk / a.n_tok);
+      return (int64_t)a.rows.len[lr] + (tk - lr * a.n_tok);
+    });
+    __syncthreads();
+    c = *reinterpret_cast<const float4 *>(s_cos + (group % kTok) * (D / 2) + 4 * sl);
+    s = *reinterpret_cast<const float4 *>(s_sin + (group % kTok) * (D / 2) + 4 * sl);
+  }
+  float wq[8], wk[8];
+  const bool nq_on = P.rope.q_norm != nullptr && v0 < nq;
+  const bool nk_on = P.rope.k_norm != nullptr && v0 < nq + nk && v1 > nq;
+  if (nq_on) {
+    load_quad(static_cast<const T *>(P.rope.q_norm) + qd.a, wq);
+    load_quad(static_cast<const T *>(P.rope.q_norm) + qd.b, wq + 4);
+  }
+  if (nk_on) {
+    load_quad(static_cast<const T *>(P.rope.k_norm) + qd.a, wk);
+    load_quad(static_cast<const T *>(P.rope.k_norm) + qd.b, wk + 4);
+  }
+  // (every group of a warp has the same vector of its own token, so what
+  // depends on the vector alone is uniform)
+  for (int base = v0; base < v1; base += SUB * kBatch) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int vu = base + i * SUB + sub;
+      if (vu < nq) {
+        if (nq_on) norm8<D>(P.rope.eps, wq, x[i]);
+      } else if (vu < nq + nk) {
+        if (nk_on) norm8<D>(P.rope.eps, wk, x[i]);
+      }
+      if (turn && vu < nq + nk) {
+        if (P.rope.interleaved) rotate8(true, c, s, x[i]);
+        else rotate8(false, c, s, x[i]);
       }
       const int vi = vec[i];
-      if constexpr (MODE == kInt4) {
-        // one vector a warp: vi is uniform
-        if (vi < 0) continue;
-        if (vi < nq) {
-          Lane<T, CPL>::store(static_cast<T *>(P.q_out) + (tok * P.Hq + vi) * D + sl * CPL, x[i]);
-          continue;
-        }
-        const bool isv = vi >= nq + nk;
-        const int kvh = vi - nq - (isv ? nk : 0);
-        const int idx = a.h.index[kvh];
+      if (MODE == kInt4 && vu >= nq && vu < v1) {
+        const bool isv = vu >= nq + nk;
+        const int kvh = vu - nq - (isv ? nk : 0);
         const bool ret = a.h.kind[kvh];
-        const int64_t row = ret ? ret_row(a.ret, b, idx, p - a.shard_lo)
-                                : ((int64_t)b * a.n_str + idx) * a.Ws + ring_slot(p, a.S, a.R);
+        const int64_t row = ret ? ret0 + a.h.index[kvh] * ret_step : str0 + (int64_t)a.h.index[kvh] * a.Ws;
         uint8_t *codes = ret ? (isv ? a.p.ret_v : a.p.ret_k) : (isv ? a.p.str_v : a.p.str_k);
-        uint8_t *sz = ret ? (isv ? a.p.ret_v_sz : a.p.ret_k_sz) : (isv ? a.p.str_v_sz : a.p.str_k_sz);
+        uint8_t *szs = ret ? (isv ? a.p.ret_v_sz : a.p.ret_k_sz) : (isv ? a.p.str_v_sz : a.p.str_k_sz);
         // rounded to bf16 first, so that the codes are those of appending
         // the rotated keys
+        uint32_t ua, ub;
+        __half2 sz;
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) x[i][j] = __bfloat162float(__float2bfloat16_rn(x[i][j]));
-        __half sch, zph;
-        const uint32_t packed = quantize_row_int4<CPL>(x[i], &sch, &zph);
-        uint8_t *dst = codes + row * (D / 2) + lane * (CPL / 2);
-        if constexpr (CPL == 4) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)packed;
-        else *dst = (uint8_t)packed;
-        if (lane == 0) {
-          __half2 pair;
-          pair.x = sch;
-          pair.y = zph;
-          reinterpret_cast<__half2 *>(sz)[row] = pair;
+        for (int j = 0; j < 8; ++j) x[i][j] = __bfloat162float(__float2bfloat16_rn(x[i][j]));
+        quantise8<D>(x[i], &ua, &ub, &sz);
+        if (vi >= 0) {
+          uint8_t *at = codes + row * (D / 2);
+          *reinterpret_cast<uint16_t *>(at + qd.a / 2) = (uint16_t)ua;
+          *reinterpret_cast<uint16_t *>(at + qd.b / 2) = (uint16_t)ub;
+          if (sl == 0) reinterpret_cast<__half2 *>(szs)[row] = sz;
         }
-      } else {
-        if (vi < 0) continue;
+      } else if (vi >= 0) {
         T *dst;
         if (vi < nq) {
           dst = static_cast<T *>(P.q_out) + (tok * P.Hq + vi) * D;
@@ -480,38 +484,35 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
           const bool isv = vi >= nq + nk;
           const int h = vi - nq - (isv ? nk : 0);
           const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
-          const int idx = a.h.index[kvh];
           if (a.h.kind[kvh])
-            dst = reinterpret_cast<T *>(isv ? a.p.ret_v : a.p.ret_k) +
-                  ret_row(a.ret, b, idx, p - a.shard_lo) * D;
+            dst = reinterpret_cast<T *>(isv ? a.p.ret_v : a.p.ret_k) + (ret0 + a.h.index[kvh] * ret_step) * D;
           else
-            dst = reinterpret_cast<T *>(isv ? a.p.str_v : a.p.str_k) +
-                  (((int64_t)b * a.n_str + idx) * a.Ws + ring_slot(p, a.S, a.R)) * D;
+            dst = reinterpret_cast<T *>(isv ? a.p.str_v : a.p.str_k) + (str0 + (int64_t)a.h.index[kvh] * a.Ws) * D;
         }
-        Lane<T, CPL>::store(dst + sl * CPL, x[i]);
+        store_quad(dst + qd.a, x[i]);
+        store_quad(dst + qd.b, x[i] + 4);
       }
     }
+    if (base + SUB * kBatch < v1) fetch(base + SUB * kBatch + sub);
   }
 }
 
 template <typename T, int D, int MODE>
-cudaError_t run(const RopeRowsParams &P, int block_ctas, cudaStream_t s) {
-  constexpr int CPL = MODE == kInt4 ? D / 32 : 8;
-  constexpr int RPW = 32 * CPL / D;
+cudaError_t run(const RopeRowsParams &P, int64_t block_ctas, cudaStream_t s) {
+  constexpr int SUB = kThreads / (D / 8) / kTok;
   const int nq = P.q.p ? P.Hq : 0;
   const int nk = MODE == kFp8Mode ? P.a.n_str : P.Hkv;
   const int64_t vecs = nq + (MODE == kAlone ? nk : 2 * nk);
-  // Vectors per warp: 4 steps share a token's angles, but a short call has
-  // too few warps then, and one step each is faster.
-  const int64_t warps4 = P.tokens * ((vecs + RPW * 4 - 1) / (RPW * 4));
-  const bool four = warps4 >= 148 * 16;
-  const int64_t warps = four ? warps4 : P.tokens * ((vecs + RPW - 1) / RPW);
-  int64_t ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  ctas = ctas < 148 * 64 ? ctas : 148 * 64;
-  const unsigned grid = (unsigned)(block_ctas + ctas);
-  if (grid == 0) return cudaSuccess;
-  if (four) rope_rows_kernel<T, D, MODE, 4><<<grid, kThreads, 0, s>>>(P, block_ctas);
-  else rope_rows_kernel<T, D, MODE, 1><<<grid, kThreads, 0, s>>>(P, block_ctas);
+  // A CTA takes all its tokens' vectors when there are tokens enough for
+  // every SM, so that each angle is formed once; else as few as its lane
+  // groups hold at once.
+  const int64_t tiles = (P.tokens + kTok - 1) / kTok;
+  int64_t per = SUB;
+  while (per < vecs && tiles * ((vecs + 2 * per - 1) / (2 * per)) >= 148 * 4) per *= 2;
+  const int64_t ctas = vecs > 0 ? tiles * ((vecs + per - 1) / per) : 0;
+  if (block_ctas + ctas == 0) return cudaSuccess;
+  if (block_ctas + ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  rope_rows_kernel<T, D, MODE><<<(unsigned)(block_ctas + ctas), kThreads, 0, s>>>(P, (int)block_ctas, (int)per);
   return cudaGetLastError();
 }
 
@@ -535,7 +536,7 @@ cudaError_t launch_append_rope(const RopeRowsParams &Pin, int kv_type, cudaStrea
   if (kv_type == kINT4) return d128 ? ra::run<bf, 128, ra::kInt4>(P, 0, s) : ra::run<bf, 64, ra::kInt4>(P, 0, s);
   if (kv_type != kFP8 || !d128) return cudaErrorInvalidValue;
   // 8-bit: per launch row one item per block that becomes full (at least
-  // one), times groups of retrieval heads
+  // one), times groups of retrieval heads, K and V apart
   int64_t items = 0;
   for (int r = 0; r < a.rows.n; ++r) {
     const int64_t len = a.rows.len[r];
@@ -549,12 +550,11 @@ cudaError_t launch_append_rope(const RopeRowsParams &Pin, int kv_type, cudaStrea
   if (items > 0 && a.n_ret > 0) {
     // several heads share a token's angles; one each while that leaves SMs idle
     while (P.heads_per_cta < a.n_ret &&
-           (int64_t)a.rows.n * items * ((a.n_ret + 2 * P.heads_per_cta - 1) / (2 * P.heads_per_cta)) >= 148 * 4)
+           2 * a.rows.n * items * ((a.n_ret + 2 * P.heads_per_cta - 1) / (2 * P.heads_per_cta)) >= 148 * 4)
       P.heads_per_cta *= 2;
-    ctas = (int64_t)a.rows.n * items * ((a.n_ret + P.heads_per_cta - 1) / P.heads_per_cta);
+    ctas = 2 * a.rows.n * items * ((a.n_ret + P.heads_per_cta - 1) / P.heads_per_cta);
   }
-  if (ctas > (1 << 30)) return cudaErrorInvalidValue;
-  return ra::run<bf, 128, ra::kFp8Mode>(P, (int)ctas, s);
+  return ra::run<bf, 128, ra::kFp8Mode>(P, ctas, s);
 }
 
 }  // namespace duo
