@@ -42,6 +42,37 @@ constexpr int kThreads = 256;
 constexpr int kTok = 4;     // tokens of a row CTA
 constexpr int kBatch = 4;   // vectors a lane group loads at once
 
+// A lane's two quads as loaded: what waits in registers for its turn.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p, int qa, int qb) {
+    a = *reinterpret_cast<const float4 *>(p + qa);
+    b = *reinterpret_cast<const float4 *>(p + qb);
+  }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int qa, int qb) {
+    a = *reinterpret_cast<const uint2 *>(p + qa);
+    b = *reinterpret_cast<const uint2 *>(p + qb);
+  }
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_f2(w[i]);
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+};
+
 // Four channels of one lane.
 __device__ __forceinline__ void load_quad(const float *p, float *x) {
   const float4 v = *reinterpret_cast<const float4 *>(p);
@@ -204,23 +235,18 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
     }
     // a head's two vectors of this half-warp; the next head's are loaded
     // before this one's are exchanged
-    auto fetch = [&](int h, float (&x)[2][8]) {
+    auto fetch = [&](int h, Raw<bf> (&x)[2]) {
       const int kvh = a.h.ret_heads[h];
       const bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const bf *p = fresh[i] ? src[i] + (int64_t)kvh * in.head : tail + (hw * 2 + i) * D;
-        if (have[i]) {
-          load_quad(p + qd.a, x[i]);
-          load_quad(p + qd.b, x[i] + 4);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-        }
+        x[i] = Raw<bf>{};
+        if (have[i]) x[i].load(p, qd.a, qd.b);
       }
     };
-    float x[2][8];
-    fetch(h0, x);
+    Raw<bf> raw[2];
+    fetch(h0, raw);
     if (part == 1) __syncthreads();  // angles and tail of part 0 are no longer read
     if (turn)
       fill_angles<D, kScaleBlock>(P.rope, s_cos, s_sin, [&](int i) {
@@ -231,12 +257,15 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       });
     __syncthreads();
     for (int h = h0; h < h1; ++h) {
-      float mx = 0.f;
+      float mx = 0.f, z[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) raw[i].unpack(z[i]);
+      if (h + 1 < h1) fetch(h + 1, raw);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[i][j];
+        for (int j = 0; j < 8; ++j) y[j] = z[i][j];
         if (norm) norm8<D>(P.rope.eps, w, y);
         if (turn) {
           const int at = (hw * 2 + i) * (D / 2) + 4 * sl;
@@ -248,16 +277,10 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // rounded to bf16 first: what the rotated keys are everywhere else
-          if (fresh[i]) x[i][j] = __bfloat162float(__float2bfloat16_rn(y[j]));
-          mx = fmaxf(mx, finite_abs(x[i][j]));
+          if (fresh[i]) z[i][j] = __bfloat162float(__float2bfloat16_rn(y[j]));
+          mx = fmaxf(mx, finite_abs(z[i][j]));
         }
       }
-      float z[2][8];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = x[i][j];
-      if (h + 1 < h1) fetch(h + 1, x);
       if (!full) {
         bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
 #pragma unroll
@@ -326,10 +349,10 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], uint32_t *qa, uin
 // Row CTAs: kTok tokens x vecs_per_cta of their head vectors: the Hq queries
 // (when given), then the K heads and, for an append, the V heads; 8-bit
 // caches list their streaming heads only.  A group of D/8 lanes keeps to one
-// token.
+// token; every group of a warp is at the same vector of its own token.
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_constant__ RopeRowsParams P,
-                                                             int block_ctas, int vecs_per_cta) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+    rope_rows_kernel(const __grid_constant__ RopeRowsParams P, int block_ctas, int vecs_per_cta) {
   constexpr int LPR = D / 8, GROUPS = kThreads / LPR, SUB = GROUPS / kTok;
   // the 8-bit mode's scale-block CTAs hold 32 tokens' angles
   constexpr int NT = MODE == kFp8Mode ? kScaleBlock : kTok;
@@ -352,68 +375,32 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
   const int nk = MODE == kFp8Mode ? a.n_str : P.Hkv;
   const int vecs = nq + (MODE == kAlone ? nk : 2 * nk);
   const int vgroups = (vecs + vecs_per_cta - 1) / vecs_per_cta;
-  const int64_t cta = (int64_t)blockIdx.x - block_ctas;
-  const int v0 = (int)(cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
-  const int64_t tok0 = cta / vgroups * kTok;
+  const int cta = (int)blockIdx.x - block_ctas;
+  const int v0 = (cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
+  const int64_t tok0 = (int64_t)(cta / vgroups) * kTok;
   const int group = threadIdx.x / LPR, sl = threadIdx.x % LPR;
-  const int64_t tok = tok0 + group % kTok;
-  const bool alive = tok < P.tokens;
+  const int sub = group / kTok;
+  const bool alive = tok0 + group % kTok < P.tokens;
+  const int64_t tok = alive ? tok0 + group % kTok : P.tokens - 1;
   const Quads qd = quads_of(P.rope, sl);
   // where the token goes in the cache: rows of its heads, one stride apart
-  int64_t p = 0, ret0 = 0, ret_step = 0, str0 = 0;
+  int64_t ret0 = 0, ret_step = 0, str0 = 0;
   bool kept_ret = true, kept_str = true;
   if constexpr (MODE != kAlone) {
-    if (alive) {
-      const int lr = (int)(tok / a.n_tok);
-      const int b = a.rows.row[lr];
-      const int64_t len = a.rows.len[lr];
-      p = len + (tok - lr * a.n_tok);
-      kept_ret = p >= a.shard_lo && p < a.shard_hi;
-      kept_str = p < a.S || p >= len + a.n_tok - a.R;
-      if (MODE != kFp8Mode && a.n_ret > 0 && kept_ret) {
-        ret0 = ret_row(a.ret, b, 0, p - a.shard_lo);
-        ret_step = a.ret.table ? kPageTokens : a.ret.cap;
-      }
-      if (kept_str) str0 = (int64_t)b * a.n_str * a.Ws + ring_slot(p, a.S, a.R);
+    const int lr = (int)(tok / a.n_tok);
+    const int b = a.rows.row[lr];
+    const int64_t len = a.rows.len[lr];
+    const int64_t p = len + (tok - lr * a.n_tok);
+    kept_ret = MODE != kFp8Mode && a.n_ret > 0 && p >= a.shard_lo && p < a.shard_hi;
+    kept_str = a.n_str > 0 && (p < a.S || p >= len + a.n_tok - a.R);
+    if (kept_ret) {
+      ret0 = ret_row(a.ret, b, 0, p - a.shard_lo);
+      ret_step = a.ret.table ? kPageTokens : a.ret.cap;
     }
-  }
-  if constexpr (MODE != kAlone) {
+    if (kept_str) str0 = (int64_t)b * a.n_str * a.Ws + ring_slot(p, a.S, a.R);
     // nothing of these tokens is kept (a long chunk's middle, streaming heads)
-    const bool any = alive && ((MODE != kFp8Mode && a.n_ret > 0 && kept_ret) || (a.n_str > 0 && kept_str));
-    if (v0 >= nq && !__syncthreads_or(any)) return;
+    if (v0 >= nq && !__syncthreads_or(alive && (kept_ret || kept_str))) return;
   }
-  // the first batch's loads are on their way while the angles are formed
-  float x[kBatch][8];
-  int vec[kBatch];  // this group's vector, -1: none
-  auto fetch = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int vi = base + i * SUB;
-      const T *src = nullptr;
-      if (alive && vi < v1) {
-        if (vi < nq) {
-          src = static_cast<const T *>(P.q.p) + tok * P.q.tok + (int64_t)vi * P.q.head;
-        } else {
-          const bool isv = vi >= nq + nk;
-          const int h = vi - nq - (isv ? nk : 0);
-          const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
-          const HeadView &in = isv ? P.v : P.k;
-          if (MODE == kAlone || (a.h.kind[kvh] ? kept_ret : kept_str))
-            src = static_cast<const T *>(in.p) + tok * in.tok + (int64_t)kvh * in.head;
-        }
-      }
-      vec[i] = src ? vi : -1;
-      if (src) {
-        load_quad(src + qd.a, x[i]);
-        load_quad(src + qd.b, x[i] + 4);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-      }
-    }
-  };
-  const int sub = group / kTok;
-  fetch(v0 + sub);
   const bool turn = P.rope.rot_dim > 0 && v0 < nq + nk;
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turn) {
@@ -427,74 +414,92 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
     c = *reinterpret_cast<const float4 *>(s_cos + (group % kTok) * (D / 2) + 4 * sl);
     s = *reinterpret_cast<const float4 *>(s_sin + (group % kTok) * (D / 2) + 4 * sl);
   }
-  float wq[8], wk[8];
-  const bool nq_on = P.rope.q_norm != nullptr && v0 < nq;
-  const bool nk_on = P.rope.k_norm != nullptr && v0 < nq + nk && v1 > nq;
-  if (nq_on) {
-    load_quad(static_cast<const T *>(P.rope.q_norm) + qd.a, wq);
-    load_quad(static_cast<const T *>(P.rope.q_norm) + qd.b, wq + 4);
-  }
-  if (nk_on) {
-    load_quad(static_cast<const T *>(P.rope.k_norm) + qd.a, wk);
-    load_quad(static_cast<const T *>(P.rope.k_norm) + qd.b, wk + 4);
-  }
-  // (every group of a warp has the same vector of its own token, so what
-  // depends on the vector alone is uniform)
-  for (int base = v0; base < v1; base += SUB * kBatch) {
+  // Vectors [first, first + count) of the token's list that this CTA takes,
+  // all of one kind: input at `in` (head stride hs), norm weights w or null;
+  // each finished vector goes to put(vector of the kind, values, ok).
+  // Everything of one batch is loaded before any of it is used.
+  auto walk = [&](int first, int count, const HeadView &view, auto head_of, const void *wp, bool rotated,
+                  auto put) {
+    const int lo = max(v0, first) - first, hi = min(v1, first + count) - first;
+    if (lo >= hi) return;
+    float w[8];
+    if (wp) {
+      load_quad(static_cast<const T *>(wp) + qd.a, w);
+      load_quad(static_cast<const T *>(wp) + qd.b, w + 4);
+    }
+    const T *in = static_cast<const T *>(view.p) + tok * view.tok;
+    for (int base = lo + sub; base < hi; base += SUB * kBatch) {
+      Raw<T> raw[kBatch];
+      bool ok[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int vu = base + i * SUB + sub;
-      if (vu < nq) {
-        if (nq_on) norm8<D>(P.rope.eps, wq, x[i]);
-      } else if (vu < nq + nk) {
-        if (nk_on) norm8<D>(P.rope.eps, wk, x[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int v = base + i * SUB;
+        const int kvh = head_of(min(v, hi - 1));
+        bool live = alive && v < hi;
+        if constexpr (MODE != kAlone)
+          if (kvh >= 0) live = live && (a.h.kind[kvh] ? kept_ret : kept_str);
+        ok[i] = live;
+        raw[i] = Raw<T>{};
+        if (live) raw[i].load(in + (int64_t)(kvh >= 0 ? kvh : v) * view.head, qd.a, qd.b);
       }
-      if (turn && vu < nq + nk) {
-        if (P.rope.interleaved) rotate8(true, c, s, x[i]);
-        else rotate8(false, c, s, x[i]);
-      }
-      const int vi = vec[i];
-      if (MODE == kInt4 && vu >= nq && vu < v1) {
-        const bool isv = vu >= nq + nk;
-        const int kvh = vu - nq - (isv ? nk : 0);
-        const bool ret = a.h.kind[kvh];
-        const int64_t row = ret ? ret0 + a.h.index[kvh] * ret_step : str0 + (int64_t)a.h.index[kvh] * a.Ws;
-        uint8_t *codes = ret ? (isv ? a.p.ret_v : a.p.ret_k) : (isv ? a.p.str_v : a.p.str_k);
-        uint8_t *szs = ret ? (isv ? a.p.ret_v_sz : a.p.ret_k_sz) : (isv ? a.p.str_v_sz : a.p.str_k_sz);
-        // rounded to bf16 first, so that the codes are those of appending
-        // the rotated keys
-        uint32_t ua, ub;
-        __half2 sz;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = __bfloat162float(__float2bfloat16_rn(x[i][j]));
-        quantise8<D>(x[i], &ua, &ub, &sz);
-        if (vi >= 0) {
-          uint8_t *at = codes + row * (D / 2);
-          *reinterpret_cast<uint16_t *>(at + qd.a / 2) = (uint16_t)ua;
-          *reinterpret_cast<uint16_t *>(at + qd.b / 2) = (uint16_t)ub;
-          if (sl == 0) reinterpret_cast<__half2 *>(szs)[row] = sz;
+      for (int i = 0; i < kBatch; ++i) {
+        const int v = base + i * SUB;
+        if (v >= hi) break;  // the same in the whole warp
+        float x[8];
+        raw[i].unpack(x);
+        if (wp) norm8<D>(P.rope.eps, w, x);
+        if (rotated) {
+          if (P.rope.interleaved) rotate8(true, c, s, x);
+          else rotate8(false, c, s, x);
         }
-      } else if (vi >= 0) {
-        T *dst;
-        if (vi < nq) {
-          dst = static_cast<T *>(P.q_out) + (tok * P.Hq + vi) * D;
-        } else if constexpr (MODE == kAlone) {
-          dst = static_cast<T *>(P.k_out) + (tok * P.Hkv + (vi - nq)) * D;
-        } else {
-          const bool isv = vi >= nq + nk;
-          const int h = vi - nq - (isv ? nk : 0);
-          const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
-          if (a.h.kind[kvh])
-            dst = reinterpret_cast<T *>(isv ? a.p.ret_v : a.p.ret_k) + (ret0 + a.h.index[kvh] * ret_step) * D;
-          else
-            dst = reinterpret_cast<T *>(isv ? a.p.str_v : a.p.str_k) + (str0 + (int64_t)a.h.index[kvh] * a.Ws) * D;
-        }
-        store_quad(dst + qd.a, x[i]);
-        store_quad(dst + qd.b, x[i] + 4);
+        put(v, x, ok[i]);
       }
     }
-    if (base + SUB * kBatch < v1) fetch(base + SUB * kBatch + sub);
-  }
+  };
+  auto write = [&](T *dst, const float (&x)[8]) {
+    store_quad(dst + qd.a, x);
+    store_quad(dst + qd.b, x + 4);
+  };
+  // cache rows of K or V heads
+  auto put_kv = [&](bool isv, int h, float (&x)[8], bool ok) {
+    const int kvh = MODE == kFp8Mode ? a.h.str_heads[h] : h;
+    const bool ret = MODE != kFp8Mode && a.h.kind[kvh];
+    const int64_t row = ret ? ret0 + a.h.index[kvh] * ret_step : str0 + (int64_t)a.h.index[kvh] * a.Ws;
+    uint8_t *base = ret ? (isv ? a.p.ret_v : a.p.ret_k) : (isv ? a.p.str_v : a.p.str_k);
+    if constexpr (MODE == kInt4) {
+      uint8_t *szs = ret ? (isv ? a.p.ret_v_sz : a.p.ret_k_sz) : (isv ? a.p.str_v_sz : a.p.str_k_sz);
+      // rounded to bf16 first, so that the codes are those of appending the
+      // rotated keys
+      uint32_t ua, ub;
+      __half2 sz;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __bfloat162float(__float2bfloat16_rn(x[j]));
+      quantise8<D>(x, &ua, &ub, &sz);
+      if (!ok) return;
+      uint8_t *at = base + row * (D / 2);
+      *reinterpret_cast<uint16_t *>(at + qd.a / 2) = (uint16_t)ua;
+      *reinterpret_cast<uint16_t *>(at + qd.b / 2) = (uint16_t)ub;
+      if (sl == 0) reinterpret_cast<__half2 *>(szs)[row] = sz;
+    } else {
+      if (ok) write(reinterpret_cast<T *>(base) + row * D, x);
+    }
+  };
+  auto no_head = [](int) { return -1; };
+  auto kv_head = [&](int h) { return MODE == kAlone ? -1 : MODE == kFp8Mode ? (int)a.h.str_heads[h] : h; };
+  walk(0, nq, P.q, no_head, P.rope.q_norm, turn, [&](int v, float (&x)[8], bool ok) {
+    if (ok) write(static_cast<T *>(P.q_out) + (tok * P.Hq + v) * D, x);
+  });
+  walk(nq, nk, P.k, kv_head, P.rope.k_norm, turn, [&](int v, float (&x)[8], bool ok) {
+    if constexpr (MODE == kAlone) {
+      if (ok) write(static_cast<T *>(P.k_out) + (tok * P.Hkv + v) * D, x);
+    } else {
+      put_kv(false, v, x, ok);
+    }
+  });
+  if constexpr (MODE != kAlone)
+    walk(nq + nk, nk, P.v, kv_head, nullptr, false,
+         [&](int v, float (&x)[8], bool ok) { put_kv(true, v, x, ok); });
 }
 
 template <typename T, int D, int MODE>
