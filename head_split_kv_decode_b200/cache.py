@@ -8,7 +8,7 @@ read and written by the library's kernels.
 import torch
 
 from . import binding as B
-from .rotary import heads_view, on_device
+from .rotary import heads_view, run_on
 
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "int4": torch.bfloat16,
                 "fp8": torch.bfloat16}
@@ -23,8 +23,9 @@ def _aligned_buffer(nbytes, device, zero):
 
 
 def _stream_handle(stream, device):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class DuoCache:
@@ -67,6 +68,7 @@ class DuoCache:
         self.ws_ptr = self._ws.data_ptr() + woff
         self.prefill_ws_bytes = B.duo_prefill_workspace_bytes(self.handle)
         self._pf_ws, self.pf_ws_ptr = None, None
+        self._regions = {}
 
     def _prefill_ws(self):
         """Pre-fill scratch (4-bit and 8-bit caches only), allocated on first use."""
@@ -124,33 +126,38 @@ class DuoCache:
         if rotary.head_dim != self.head_dim:
             raise ValueError("rotary is for head_dim %d, the cache's is %d"
                              % (rotary.head_dim, self.head_dim))
-        desc = rotary.desc(self.io_dtype, self.device)
+        io, dev = self.io_dtype, self.device
+        desc = rotary.desc(io, dev)
         kv_shape = (n_rows, n, self.n_kv_heads, self.head_dim)
-        kh = heads_view(k, kv_shape, "k", self.io_dtype, self.device)
-        vh = heads_view(v, kv_shape, "v", self.io_dtype, self.device)
-        qh, qo_ptr, pos_ptr = None, None, None
-        with on_device(self.device, stream) as s:
-            if q is not None:
-                q_shape = (n_rows, n, self.n_q_heads, self.head_dim)
-                qh = heads_view(q, q_shape, "q", self.io_dtype, self.device)
-                if q_out is None:
-                    q_out = torch.empty(q_shape, dtype=self.io_dtype, device=self.device)
+        kh = heads_view(k, kv_shape, "k", io, dev)
+        vh = heads_view(v, kv_shape, "v", io, dev)
+        qh, q_shape, pos_ptr = None, (n_rows, n, self.n_q_heads, self.head_dim), None
+        if q is not None:
+            qh = heads_view(q, q_shape, "q", io, dev)
+            if q_out is not None:
                 self._check(q_out, q_shape, "q_out")
-                qo_ptr = q_out.data_ptr()
-            elif q_out is not None:
-                raise ValueError("q_out without q")
-            if positions is not None:
-                self._check(positions, (n_rows, n), "positions", torch.int64)
-                pos_ptr = positions.data_ptr()
-            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh, kh, vh, pos_ptr, n, qo_ptr, s)
-        return q_out
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if positions is not None:
+            self._check(positions, (n_rows, n), "positions", torch.int64)
+            pos_ptr = positions.data_ptr()
+
+        def call(handle):
+            out = q_out
+            if qh is not None and out is None:
+                out = q.new_empty(q_shape)
+            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh, kh, vh, pos_ptr, n,
+                                   None if out is None else out.data_ptr(), handle)
+            return out
+
+        return run_on(dev, stream, call)
 
     def decode(self, layer, q, out=None, scale=0.0, stream=None):
         """q: [batch, n_q_heads, head_dim] at position seq_len-1.  Returns out."""
         shape = (self.batch, self.n_q_heads, self.head_dim)
         self._check(q, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=self.out_dtype, device=q.device)
+            out = q.new_empty(shape, dtype=self.out_dtype)
         self._check(out, shape, "out", self.out_dtype)
         B.duo_decode_attn(self.handle, layer, q.data_ptr(), out.data_ptr(), float(scale),
                           self.ws_ptr, self.ws_bytes, _stream_handle(stream, self.device))
@@ -165,7 +172,7 @@ class DuoCache:
         self._check(k_new, kv_shape, "k_new")
         self._check(v_new, kv_shape, "v_new")
         if out is None:
-            out = torch.empty(shape, dtype=self.out_dtype, device=q.device)
+            out = q.new_empty(shape, dtype=self.out_dtype)
         self._check(out, shape, "out", self.out_dtype)
         B.duo_decode_step(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
                           out.data_ptr(), float(scale), self.ws_ptr, self.ws_bytes,
@@ -210,7 +217,7 @@ class DuoCache:
         shape = (len(rows), self.n_q_heads, self.head_dim)
         self._check(q, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=self.out_dtype, device=q.device)
+            out = q.new_empty(shape, dtype=self.out_dtype)
         self._check(out, shape, "out", self.out_dtype)
         B.duo_decode_attn_rows(self.handle, layer, rows, q.data_ptr(), out.data_ptr(), float(scale),
                                self.ws_ptr, self.ws_bytes, _stream_handle(stream, self.device))
@@ -225,7 +232,7 @@ class DuoCache:
         self._check(k_new, kv_shape, "k_new")
         self._check(v_new, kv_shape, "v_new")
         if out is None:
-            out = torch.empty(shape, dtype=self.out_dtype, device=q.device)
+            out = q.new_empty(shape, dtype=self.out_dtype)
         self._check(out, shape, "out", self.out_dtype)
         B.duo_decode_step_rows(self.handle, layer, rows, q.data_ptr(), k_new.data_ptr(),
                                v_new.data_ptr(), out.data_ptr(), float(scale), self.ws_ptr,
@@ -326,6 +333,12 @@ class DuoCache:
         Returns a uint8 tensor [batch, heads, rows, row_bytes] (or [..., 4]);
         paged retrieval buffers are [pool_blocks, heads, page_tokens, ...].
         """
+        key = layer, name
+        if key not in self._regions:  # where a buffer lies never changes
+            self._regions[key] = self._region(layer, name)
+        return self._regions[key]
+
+    def _region(self, layer, name):
         lv = self.layout(layer)
         fp8 = self.kv_dtype == "fp8"
         if name.startswith("tail"):

@@ -5,27 +5,23 @@ PyTorch is used for device memory and streams only; the arithmetic runs in the
 library's kernels.
 """
 
-import contextlib
-import ctypes
-
 import torch
 
 from . import binding as B
 
-_DTYPE = {torch.bfloat16: "bf16", torch.float32: "f32"}
+_DTYPE = {torch.bfloat16: B.DUO_BF16, torch.float32: B.DUO_F32}
+_BYTES = {torch.bfloat16: 2, torch.float32: 4}
 
 
-@contextlib.contextmanager
-def on_device(device, stream):
-    """Make ``device`` (and ``stream``, so that outputs allocated inside belong
-    to it) current for a call; yields the stream's handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream(device).cuda_stream
-        return
+def run_on(device, stream, call):
+    """call(stream handle) with ``device``, and ``stream`` (default the
+    device's current one), current: what it allocates belongs to that stream."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         s = stream if stream is not None else torch.cuda.current_stream(device)
         with torch.cuda.stream(s):
-            yield s.cuda_stream
+            return call(s.cuda_stream)
 
 
 def heads_view(t, shape, name, dtype, device):
@@ -35,31 +31,30 @@ def heads_view(t, shape, name, dtype, device):
         raise TypeError("%s must be a torch tensor" % name)
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.numel() == 0:  # nothing to read
+    ptr, st = t.data_ptr(), t.stride()
+    if ptr == 0:  # nothing to read
         return B.duo_heads(None, 0, 0)
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    if st[-1] != 1:
         raise ValueError("%s must have contiguous channels" % name)
     # one stride for all tokens: the innermost leading dimension's, which the
     # outer ones have to continue
     tok, count = 0, 1
-    for size, stride in zip(reversed(shape[:-2]), reversed(st[:-2])):
-        if size == 1:
+    for i in range(len(shape) - 3, -1, -1):
+        if shape[i] == 1:
             continue
         if count == 1:
-            tok = stride
-        elif stride != tok * count:
+            tok = st[i]
+        elif st[i] != tok * count:
             raise ValueError("%s: its tokens must lie at one stride" % name)
-        count *= size
+        count *= shape[i]
     head = st[-2] if shape[-2] > 1 else 0
-    step = 16 // t.element_size()
-    if t.data_ptr() % 16 or tok % step or head % step:
+    if (ptr | tok * _BYTES[dtype] | head * _BYTES[dtype]) & 15:
         raise ValueError("%s must start at, and its tokens and heads lie at, multiples of 16 bytes" % name)
-    return B.duo_heads(t.data_ptr(), tok, head)
+    return B.duo_heads(ptr, tok, head)
 
 
 class Rotary:
@@ -99,9 +94,12 @@ class Rotary:
 
         self._desc = B.duo_rope_desc(self.rot_dim, int(bool(interleaved)), ptr(inv_freq),
                                      float(mscale), float(eps), ptr(q_norm), ptr(k_norm))
+        self._checked = None  # the last (dtype, device) found right
 
     def desc(self, dtype, device):
         """The C description, for tensors of dtype on device."""
+        if self._checked == (dtype, device):
+            return self._desc
         for name, t in (("inv_freq", self.inv_freq), ("q_norm", self.q_norm), ("k_norm", self.k_norm)):
             if t is None:
                 continue
@@ -109,6 +107,7 @@ class Rotary:
                 raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
             if name != "inv_freq" and t.dtype != dtype:
                 raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+        self._checked = dtype, device
         return self._desc
 
 
@@ -120,41 +119,44 @@ def qk_norm_rope(rotary, q, k, positions=None, q_out=None, k_out=None, stream=No
     ref = q if q is not None else k
     if not isinstance(ref, torch.Tensor) or ref.dim() < 3:
         raise ValueError("q or k must be a [..., heads, head_dim] tensor")
-    dtype, device, lead = ref.dtype, ref.device, tuple(ref.shape[:-2])
-    if dtype not in _DTYPE:
+    dtype, device, lead = ref.dtype, ref.device, ref.shape[:-2]
+    kind = _DTYPE.get(dtype)
+    if kind is None:
         raise ValueError("q and k must be bfloat16 or float32")
     if device.type != "cuda":
         raise ValueError("q and k must be CUDA tensors")
     desc = rotary.desc(dtype, device)
-    n = 1
-    for size in lead:
-        n *= size
+    pos_ptr = None
     if positions is not None:
-        if (not isinstance(positions, torch.Tensor) or positions.dtype != torch.int64
-                or positions.device != device or tuple(positions.shape) != lead
+        if (not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int64
+                or positions.device != device or positions.shape != lead
                 or not positions.is_contiguous()):
-            raise ValueError("positions must be a contiguous int64 tensor %s on %s" % (lead, device))
+            raise ValueError("positions must be a contiguous int64 tensor %s on %s" % (tuple(lead), device))
+        pos_ptr = positions.data_ptr()
     elif rotary.rot_dim:
         raise ValueError("positions are needed to rotate")
-    with on_device(device, stream) as s:
-        views, outs, heads = [], [], []
-        for name, t, out in (("q", q, q_out), ("k", k, k_out)):
-            if t is None:
-                if out is not None:
-                    raise ValueError("%s_out without %s" % (name, name))
-                views.append(None), outs.append(None), heads.append(0)
-                continue
-            shape = lead + (t.shape[-2] if t.dim() == ref.dim() else -1, rotary.head_dim)
-            views.append(heads_view(t, shape, name, dtype, device))
-            if out is None:
-                out = torch.empty(shape, dtype=dtype, device=device)
-            elif (out.device != device or tuple(out.shape) != shape or out.dtype != dtype
-                  or not out.is_contiguous()):
-                raise ValueError("%s_out must be a contiguous %s tensor %s on %s" % (name, dtype, shape, device))
-            outs.append(out)
-            heads.append(t.shape[-2])
-        B.duo_qk_norm_rope(desc, _DTYPE[dtype], n, heads[0], heads[1], rotary.head_dim, views[0],
-                           views[1], None if positions is None else positions.data_ptr(),
-                           None if outs[0] is None else outs[0].data_ptr(),
-                           None if outs[1] is None else outs[1].data_ptr(), s)
-    return outs[0], outs[1]
+
+    def call(handle):
+        qh, qo, qp, nq = _side("q", q, q_out, lead, rotary.head_dim, dtype, device)
+        kh, ko, kp, nk = _side("k", k, k_out, lead, rotary.head_dim, dtype, device)
+        B.duo_qk_norm_rope(desc, kind, lead.numel(), nq, nk, rotary.head_dim, qh, kh, pos_ptr, qp, kp,
+                           handle)
+        return qo, ko
+
+    return run_on(device, stream, call)
+
+
+def _side(name, t, out, lead, head_dim, dtype, device):
+    """(view, output, its pointer, heads) of q or k; the output is allocated when not given."""
+    if t is None:
+        if out is not None:
+            raise ValueError("%s_out without %s" % (name, name))
+        return None, None, None, 0
+    heads = t.shape[-2] if t.dim() > 1 else 0
+    shape = lead + (heads, head_dim)
+    view = heads_view(t, shape, name, dtype, device)
+    if out is None:
+        out = t.new_empty(shape)
+    elif out.device != device or out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
+        raise ValueError("%s_out must be a contiguous %s tensor %s on %s" % (name, dtype, tuple(shape), device))
+    return view, out, out.data_ptr(), heads
