@@ -864,6 +864,8 @@ size_t prefill_ws_bytes(const duo_cache *c) {
   if (c->desc.kv_dtype != DUO_INT4 && c->desc.kv_dtype != DUO_FP8) return 0;
   int64_t m = 0;
   for (int l = 0; l < c->desc.layers; ++l) m = std::max(m, prefill_scratch(c, l).total);
+  // 8-bit: the partials of a split pre-fill follow the expansion
+  if (is_fp8(c)) m = round_up(m, kAlign) + (int64_t)duo::prefill_split_bytes();
   return (size_t)m;
 }
 
@@ -936,6 +938,9 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
   p.wait_ns = c->stall_ns > 0 ? (uint64_t)c->stall_ns : duo::kPrefillWaitNs;
   p.skip_loads = c->stall_ns > 0 ? 1 : 0;
   c->stall_ns = 0;  // one call only
+  duo::DecodeConfig cfg{};  // for its SM count
+  if (is_fp8(c) && cached_decode_config(c, &cfg) != cudaSuccess) return DUO_ERR_CUDA;
+  uint8_t *split_ws = is_fp8(c) ? wsb + prefill_ws_bytes(c) - duo::prefill_split_bytes() : nullptr;
   const int64_t q_row = (int64_t)C * d.n_q_heads * d.head_dim * 2;
   const int64_t kv_row = (int64_t)C * d.n_kv_heads * d.head_dim * 2;
   for (size_t g0 = 0; g0 < rows.size(); g0 += duo::kMaxLaunchRows) {
@@ -956,7 +961,9 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
                     : duo::launch_dequant_history(dq, s);
       if ((st = cuda_status(e)) != DUO_OK) return st;
     }
-    if ((st = launch_status(duo::launch_prefill(p, s))) != DUO_OK) return st;
+    const int ns = is_fp8(c) ? duo::prefill_splits(p, cfg.num_sms) : 1;
+    const cudaError_t e = ns > 1 ? duo::launch_prefill_split(p, ns, split_ws, s) : duo::launch_prefill(p, s);
+    if ((st = launch_status(e)) != DUO_OK) return st;
   }
   return DUO_OK;
 }

@@ -60,6 +60,15 @@ struct DequantFp8Params {
   TailPtrs tail;
 };
 
+// Pre-fill with a retrieval item's tiles cut into ns runs: each run's
+// normalised output [256][128] and log-sum-exp (base 2) [256], by CTA.
+struct PrefillSplit {
+  float *o, *lse;
+  int ns;
+};
+// Most retrieval CTAs of a split pre-fill (twice the SMs): bounds its workspace.
+constexpr int kPrefillSplitCtas = 296;
+
 cudaError_t launch_qk_norm_rope(const RopeRowsParams &p, int io_type, int D, cudaStream_t s);
 cudaError_t launch_append_rope(const RopeRowsParams &p, int kv_type, cudaStream_t s);
 cudaError_t launch_dequant_fp8(const DequantFp8Params &p, cudaStream_t s);
@@ -68,5 +77,9 @@ cudaError_t decode_fp8_config(int G, DecodeConfig *cfg);
 cudaError_t launch_decode_fp8(const DecodeFp8Params &p, cudaStream_t s);
 // Keys a CTA of the 8-bit decode walks per iteration; host only.
 int decode_fp8_tile_rows();
+
+int prefill_splits(const PrefillParams &p, int num_sms);  // 1: do not split
+size_t prefill_split_bytes();
+cudaError_t launch_prefill_split(const PrefillParams &p, int ns, void *ws, cudaStream_t s);
 
 }  // namespace duo

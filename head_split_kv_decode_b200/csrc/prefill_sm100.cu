@@ -19,11 +19,18 @@
 // S, P and O live in tensor memory (4 x 128 columns); O is rescaled in TMEM only
 // when a row's running max grows by more than 2^8 (the ratio stays exact).
 // Both query tiles share every K/V tile; K/V are double buffered.
+//
+// A short chunk on a long history has few (head, query pair) items, each a
+// long walk: with SPLIT a retrieval item's tiles are cut into ns runs, one CTA
+// each, that leave normalised partials and log-sum-exps in a workspace, and a
+// second kernel merges them.  (8-bit caches only: their pre-fill has a
+// workspace anyway.)
 #include <cuda.h>
 
 #include <cstring>
 
 #include "common.cuh"
+#include "kv8.h"
 
 namespace duo {
 
@@ -285,8 +292,10 @@ struct Maps {
 
 __device__ __forceinline__ bool abort_set(volatile int *flag) { return *flag != 0; }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_kernel(const __grid_constant__ PrefillParams P, const __grid_constant__ Maps M) {
+    prefill_kernel(const __grid_constant__ PrefillParams P, const __grid_constant__ Maps M,
+                   const __grid_constant__ PrefillSplit X) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -302,6 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int blk = blockIdx.x;
   bool retrieval;
   int b, hq, kvh, pidx, pair;  // b: launch row (indexes the inputs and outputs)
+  int split = 0;
+  if constexpr (SPLIT) {
+    const int ret_ctas = P.rows.n * ret_q * n_pairs * X.ns;
+    if (blk < ret_ctas) {
+      split = blk % X.ns;
+      blk /= X.ns;
+    } else {
+      blk -= ret_ctas - P.rows.n * ret_q * n_pairs;
+    }
+  }
   if (blk < P.rows.n * ret_q * n_pairs) {
     retrieval = true;
     const int per = P.rows.n * ret_q;
@@ -329,7 +348,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = pair * 2 * BM;
   Sched sc;
   sc.init(retrieval, c0, P.C, P.S, P.R, P.W, q0);
-  const int n_tiles = sc.count();
+  int n_tiles = sc.count(), j0 = 0;  // tiles [j0, j0 + n_tiles) of the item's list
+  if constexpr (SPLIT) {
+    if (retrieval) {
+      const int all = n_tiles;
+      j0 = (int)((int64_t)all * split / X.ns);
+      n_tiles = (int)((int64_t)all * (split + 1) / X.ns) - j0;
+      if (n_tiles == 0) {  // a short row's item has fewer tiles than runs
+        if (tid < 2 * BM) X.lse[(int64_t)blockIdx.x * (2 * BM) + tid] = -INFINITY;
+        return;
+      }
+    }
+  }
 
   // ---- set-up: barriers, tensor memory
   if (tid == 0) {
@@ -375,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  P.err, kErrWaitPrefillLoad, P.wait_ns))
           return false;
         int seg, idx;
-        sc.get(j, seg, idx);
+        sc.get(SPLIT ? j0 + j : j, seg, idx);
         const uint32_t dst = base + (is_v ? (st ? kV1 : kV0) : (st ? kK1 : kK0));
         const uint32_t fb = bar((is_v ? V_FULL0 : K_FULL0) + st);
         mbar_arrive_expect_tx(fb, TILE);
@@ -511,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       int seg, idx;
-      sc.get(j, seg, idx);
+      sc.get(SPLIT ? j0 + j : j, seg, idx);
 
       // Visible columns of this row as bit masks, one per 32 columns.  Every
       // visible set here is a union of at most three position ranges.
@@ -639,7 +669,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int cc = 0; cc < HD / 32; ++cc) tmem_ld32_async(tO + 32u * cc, o + 32 * cc);
       tmem_wait_ld();
-      if (crow < P.C) {
+      if (SPLIT && retrieval) {
+        const int64_t at = (int64_t)blockIdx.x * (2 * BM) + x * BM + row;
+        if (crow < P.C) {
+          float4 *dst = reinterpret_cast<float4 *>(X.o + at * HD);
+#pragma unroll
+          for (int i = 0; i < HD / 4; ++i)
+            dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          X.lse[at] = l > 0.f ? m + fast_log2(l) : -INFINITY;
+        }
+      } else if (crow < P.C) {
         uint4 *dst = reinterpret_cast<uint4 *>(out);
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
@@ -701,10 +740,51 @@ static bool make_map(CUtensorMap *m, const void *ptr, uint64_t d1, uint64_t d2, 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Merge of a split item's partials: one warp per (query, retrieval query
+// head), four channels a lane.  Bound: HBM or L2, ns * 516 bytes read and 256
+// written per query and head.
+__global__ void prefill_merge_kernel(const __grid_constant__ PrefillParams P,
+                                     const __grid_constant__ PrefillSplit X) {
+  const int n_pairs = (P.C + 2 * BM - 1) / (2 * BM);
+  const int ret_q = P.n_ret * P.G, per = P.rows.n * ret_q;
+  const int lane = threadIdx.x & 31;
+  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (w >= (int64_t)per * P.C) return;
+  const int crow = (int)(w % P.C), r = (int)(w / P.C);  // r = launch row * ret_q + query head
+  const int pair = crow / (2 * BM);
+  const int item = (n_pairs - 1 - pair) * per + r;
+  const int64_t at = ((int64_t)item * X.ns) * (2 * BM) + crow % (2 * BM);
+  float M = -INFINITY;
+  for (int i = 0; i < X.ns; ++i) M = fmaxf(M, __ldcg(X.lse + at + (int64_t)i * (2 * BM)));
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < X.ns; ++i) {
+    const int64_t k = at + (int64_t)i * (2 * BM);
+    const float e = __ldcg(X.lse + k);
+    if (e == -INFINITY) continue;  // this run saw no key of the query
+    const float g = fast_exp2(e - M);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(X.o + k * HD) + lane);
+    den += g;
+    acc.x = fmaf(g, v.x, acc.x), acc.y = fmaf(g, v.y, acc.y);
+    acc.z = fmaf(g, v.z, acc.z), acc.w = fmaf(g, v.w, acc.w);
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int rr = r % ret_q;
+  const int hq = P.h.ret_heads[rr / P.G] * P.G + rr % P.G;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(P.out) +
+                       (((int64_t)(r / ret_q) * P.C + crow) * P.Hq + hq) * HD;
+  reinterpret_cast<uint2 *>(out)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
 }  // namespace pf
 
-cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
-  using namespace pf;
+namespace pf {
+
+template <bool SPLIT>
+static cudaError_t launch(const PrefillParams &p, const PrefillSplit &x, cudaStream_t s) {
   if (p.D != HD || p.C <= 0) return cudaErrorInvalidValue;
   Maps maps;
   std::memset(&maps, 0, sizeof(maps));
@@ -729,20 +809,64 @@ cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<SPLIT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // The register split must fit the registers the CTA is launched with, or
     // setmaxnreg.inc would wait for registers that never come.
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, prefill_kernel)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, prefill_kernel<SPLIT>)) != cudaSuccess) return e;
     if (128 * (2 * kRegsHigh + kRegsLow) > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
     attr = true;
   }
   const int n_pairs = (p.C + 2 * BM - 1) / (2 * BM);
-  const int grid = p.rows.n * (p.n_ret + p.n_str) * p.G * n_pairs;
-  prefill_kernel<<<grid, kThreads, kSmemBytes, s>>>(p, maps);
+  const int grid = p.rows.n * (p.n_ret * (SPLIT ? x.ns : 1) + p.n_str) * p.G * n_pairs;
+  prefill_kernel<SPLIT><<<grid, kThreads, kSmemBytes, s>>>(p, maps, x);
+  cudaError_t e = cudaGetLastError();
+  if (!SPLIT || e != cudaSuccess) return e;
+  const int64_t warps = (int64_t)p.rows.n * p.n_ret * p.G * p.C;
+  prefill_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p, x);
   return cudaGetLastError();
+}
+
+}  // namespace pf
+
+cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
+  return pf::launch<false>(p, PrefillSplit{}, s);
+}
+
+// How many runs a retrieval item's tiles are cut into.  Measured: a CTA (one
+// per SM) takes about 2.4 us per tile of its pair of query tiles; the merge
+// costs about 4 us and its partials' bytes.  The fewest waves of the longest
+// run win, if they save a tenth.
+int prefill_splits(const PrefillParams &p, int num_sms) {
+  using namespace pf;
+  const int n_pairs = (p.C + 2 * BM - 1) / (2 * BM);
+  const int64_t items = (int64_t)p.rows.n * p.n_ret * p.G * n_pairs;
+  int64_t len = 0;
+  for (int r = 0; r < p.rows.n; ++r) len = len > p.rows.len[r] ? len : p.rows.len[r];
+  const int64_t tiles = (len + BN - 1) / BN + (p.C + BN - 1) / BN;
+  if (items == 0 || num_sms <= 0) return 1;
+  double best = 0.0, whole = 0.0;
+  int ns = 1;
+  for (int k = 1; k <= tiles && items * k <= kPrefillSplitCtas; ++k) {
+    const int64_t waves = (items * k + num_sms - 1) / num_sms;
+    double t = 2.4 * (double)waves * (double)((tiles + k - 1) / k);
+    if (k > 1) t += 4.0 + (double)(items * k) * (2 * BM * (HD + 1) * 4.0 * 2.0) / 5e6;
+    if (k == 1) whole = best = t;
+    else if (t < best && t < 0.9 * whole) best = t, ns = k;
+  }
+  return ns;
+}
+
+size_t prefill_split_bytes() { return (size_t)kPrefillSplitCtas * 2 * pf::BM * (pf::HD + 1) * sizeof(float); }
+
+cudaError_t launch_prefill_split(const PrefillParams &p, int ns, void *ws, cudaStream_t s) {
+  PrefillSplit x;
+  x.ns = ns;
+  x.o = static_cast<float *>(ws);
+  x.lse = x.o + (size_t)kPrefillSplitCtas * 2 * pf::BM * pf::HD;
+  return pf::launch<true>(p, x, s);
 }
 
 }  // namespace duo

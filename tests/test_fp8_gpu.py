@@ -365,6 +365,34 @@ def test_prefill(cuda_lib, h, C, paged):
         assert_parity(out[b:b + 1], ref, "bf16", "row %d" % b)
 
 
+@pytest.mark.parametrize("lens,C,hq,hkv,n_ret", [
+    ([4000], 7, 8, 2, 1), ([3000], 300, 8, 4, 2), ([5000, 40], 20, 4, 2, 1), ([1, 2000, 130], 129, 6, 2, 2),
+    ([2500], 1, 16, 2, 1)])
+def test_prefill_split(cuda_lib, lens, C, hq, hkv, n_ret):
+    """Short chunks on long histories, whose tiles are cut into runs (rows with
+    fewer tiles than runs among them), against the oracle."""
+    S, R, batch = 4, 60, len(lens)
+    cache, mask = _cache(batch, hq, hkv, n_ret, max(lens) + C, S, R, paged=batch > 1)
+
+    def plain(seed, n, heads):
+        return synth.kv_field(seed, [0], range(n), heads, D, device="cuda")[0].to(BF)
+    K = [plain(10 + b, n + C, hkv) for b, n in enumerate(lens)]
+    V = [plain(20 + b, n + C, hkv) for b, n in enumerate(lens)]
+    q = [plain(30 + b, C, hq) for b in range(batch)]
+    for b, n in enumerate(lens):
+        cache.append_rows(0, [b], K[b][None, :n], V[b][None, :n])
+    cache._prefill_ws()
+    cache._pf_ws.fill_(0xFF)
+    out = cache.prefill(0, torch.stack(q), torch.stack([x[n:] for x, n in zip(K, lens)]),
+                        torch.stack([x[n:] for x, n in zip(V, lens)]))
+    torch.cuda.synchronize()
+    assert B.duo_poll_device_error() == 0
+    for b, h in enumerate(lens):
+        kh, vh = (np.concatenate([_held(x[:h], mask)[0], f64(x[h:])]) for x in (K[b], V[b]))
+        ref = OA.prefill_reference(f64(q[b])[None], kh[None], vh[None], h, mask.numpy(), S, R)
+        assert_parity(out[b:b + 1], ref, "bf16", "row %d" % b)
+
+
 def test_calls_refused(cuda_lib):
     cache, mask = _cache(1, 8, 2, 1, 256)
     q = _seq(1, 1, 8)
