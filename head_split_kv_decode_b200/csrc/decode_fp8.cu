@@ -481,7 +481,6 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         }
         // the first claim is issued during the share's last tile
         if (pooled && tt + NWARPS >= t1 && lane == 0) c = atomicAdd(next, 1u);
-        if (!P.ret.table && lane == 0 && tt + NWARPS < t1) prefetch_tile(tt + NWARPS);
         tile_fp8(tt);
         tt += NWARPS;
       } else {
