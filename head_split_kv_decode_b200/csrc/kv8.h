@@ -47,6 +47,7 @@ struct RopeRowsParams {
   // 8-bit cache: CTAs of scale blocks in front of the row CTAs
   int block_items;            // scale-block items per (row, head group), at most over rows
   int heads_per_cta;          // retrieval heads one scale-block CTA walks
+  int tails_in_rows;          // no row completes a block: the row CTAs write the tails
 };
 
 struct DecodeFp8Params {

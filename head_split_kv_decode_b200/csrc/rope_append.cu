@@ -7,9 +7,8 @@
 //   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s) for every rotated pair (a, b),
 //   c + i s = mscale * e^(i * position * inv_freq[pair]).
 // All of it in fp32, rounded once to the input's type.  The angle is formed in
-// 64 bits: at position 10^6 a 32-bit product is off by up to 0.06 radian.  As
-// a fraction of a turn it is then reduced exactly to [-1/2, 1/2] and only
-// that is rounded to fp32 (off by at most 2^-25 of a turn).  Pages: "What is
+// 64 bits, as a fixed-point fraction of a turn: at position 10^6 a 32-bit
+// floating-point product is off by up to 0.06 radian.  Pages: "What is
 // DuoAttention" (nav.superapi.store), section "Technical principles of
 // DuoAttention" (what each kind of head keeps); the pages leave positions to
 // the model.
@@ -104,25 +103,73 @@ __device__ __forceinline__ Quads quads_of(const RopeParams &r, int sl) {
   return {8 * sl, 8 * sl + 4};
 }
 
-// mscale * (cos, sin) of pair `pair` at position pos.
-__device__ __forceinline__ float2 angle(const RopeParams &r, double pos_turns, int pair) {
-  const double turns = pos_turns * (double)r.inv_freq[pair];
-  float s, c;
-  sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-  return make_float2(c * r.mscale, s * r.mscale);
+// inv_freq / (2 pi) as a 64-bit fraction of a turn, modulo whole turns: the
+// 24-bit significand times the leading 64 bits of 1 / (2 pi) (scaled by 2^66),
+// shifted by the exponent.  Off by at most 2 units of 2^-64.
+__device__ __forceinline__ uint64_t turn_rate(float inv_freq) {
+  constexpr uint64_t kInvTwoPi = 0xA2F9836E4E441529ull;
+  const uint32_t u = __float_as_uint(inv_freq);
+  const int e = (u >> 23) & 0xff;
+  const uint64_t m = (u & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int sh = 152 - max(e, 1);
+  const uint64_t hi = __umul64hi(m, kInvTwoPi), lo = m * kInvTwoPi;
+  uint64_t f;
+  if (sh >= 64) f = sh < 128 ? hi >> (sh - 64) : 0;
+  else if (sh > 0) f = lo >> sh | hi << (64 - sh);
+  else f = sh > -64 ? lo << -sh : 0;
+  return u >> 31 ? 0 - f : f;
 }
-constexpr double kPerTurn = 0.15915494309189533576888;  // 1 / (2 pi)
 
-// Sines and cosines of NT tokens into shared memory, [token][D/2] each; pairs
-// past rot_dim/2 turn by nothing.  pos(i) gives token i's position.
+// (cos, sin) of pos * rate turns.  The product modulo 2^64 is the turn's
+// fraction with nothing lost (a far position keeps its phase); its upper half
+// is split into the nearest quarter turn and a rest of at most pi/4, whose
+// sine and cosine are their Taylor sums (the first terms left out are below
+// 2e-9 and 3e-8).  Integer and fp32 pipes only: 64-bit floating-point
+// conversions run at a sixteenth of the rate.
+__device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t rate) {
+  const uint32_t t = (uint32_t)(((uint64_t)pos * rate) >> 32);
+  const uint32_t q = (t + 0x20000000u) >> 30;  // nearest quarter turn
+  const float x = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
+  s = fmaf(z, s, 8.3333333e-3f);                     // 1/5!
+  s = fmaf(z, s, -0.16666667f);                      // -1/3!
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, 2.4801587e-5f, -1.3888889e-3f);  // 1/8!, -1/6!
+  c = fmaf(z, c, 4.1666667e-2f);                     // 1/4!
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;
+  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+  return make_float2(__uint_as_float(__float_as_uint(a) ^ (((q + 1) & 2) << 30)),
+                     __uint_as_float(__float_as_uint(b) ^ ((q & 2) << 30)));
+}
+
+// mscale * cosines and sines of NT tokens into shared memory, [token][D/2]
+// each; pairs past rot_dim/2 turn by nothing.  pos(i, p) puts token i's
+// position into p, or returns false: its angles are not needed.  The
+// positions are all read before any is used.
 template <int D, int NT, typename PosFn>
 __device__ __forceinline__ void fill_angles(const RopeParams &r, float *s_cos, float *s_sin, PosFn pos) {
-  for (int i = threadIdx.x; i < NT * (D / 2); i += kThreads) {
-    const int pair = i % (D / 2);
-    float2 cs = make_float2(1.f, 0.f);
-    if (pair < (r.rot_dim >> 1)) cs = angle(r, (double)pos(i / (D / 2)) * kPerTurn, pair);
-    s_cos[i] = cs.x;
-    s_sin[i] = cs.y;
+  constexpr int kPer = kThreads / (D / 2), kIt = (NT + kPer - 1) / kPer;  // tokens at once, rounds
+  static_assert(kThreads % (D / 2) == 0, "a thread keeps to one pair");
+  const int pair = threadIdx.x % (D / 2), first = threadIdx.x / (D / 2);
+  int64_t p[kIt];
+  bool need[kIt];
+#pragma unroll
+  for (int k = 0; k < kIt; ++k) {
+    p[k] = 0;
+    need[k] = first + k * kPer < NT && pos(first + k * kPer, p[k]);
+  }
+  const bool turns = pair < (r.rot_dim >> 1);
+  const uint64_t rate = turns ? turn_rate(r.inv_freq[pair]) : 0;
+#pragma unroll
+  for (int k = 0; k < kIt; ++k) {
+    if (!need[k]) continue;
+    float2 cs = cos_sin(p[k], rate);
+    if (turns) cs.x *= r.mscale, cs.y *= r.mscale;
+    s_cos[threadIdx.x + k * kThreads] = cs.x;  // pair's column of token first + k * kPer
+    s_sin[threadIdx.x + k * kThreads] = cs.y;
   }
 }
 
@@ -259,13 +306,16 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
     };
     Raw<bf> raw[2];
     fetch(h0, raw);
+    // (a table entry is read once for all heads; an open block's is not needed)
+    const int64_t row0 = full ? ret_row(a.ret, b, 0, first) : 0;
+    const int64_t head_step = a.ret.table ? kPageTokens : a.ret.cap;
     if (part == 1) __syncthreads();  // angles and tail of part 0 are no longer read
     if (turn)
-      fill_angles<D, kScaleBlock>(P.rope, s_cos, s_sin, [&](int i) {
+      fill_angles<D, kScaleBlock>(P.rope, s_cos, s_sin, [&](int i, int64_t &p) {
         const int64_t t = t0 + i;
-        // older tokens (and those past the call's) are not rotated
-        if (t < 0 || t >= a.n_tok) return (int64_t)0;
-        return P.positions ? P.positions[tok0 + i] : len + t;
+        if (t < 0 || t >= a.n_tok) return false;  // not the call's
+        p = P.positions ? P.positions[tok0 + i] : len + t;
+        return true;
       });
     __syncthreads();
     for (int h = h0; h < h1; ++h) {
@@ -312,7 +362,7 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       buf ^= 1;
       const int e = scale_exp(mx);
       const float inv = pow2i(-e);
-      const int64_t row = ret_row(a.ret, b, h, first);
+      const int64_t row = row0 + h * head_step;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint8_t *at = codes + (row + hw * 2 + i) * D;
@@ -359,7 +409,7 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], uint32_t *qa, uin
 
 // Row CTAs: kTok tokens x vecs_per_cta of their head vectors: the Hq queries
 // (when given), then the K heads and, for an append, the V heads; 8-bit
-// caches list their streaming heads only, and no list holds streaming heads
+// caches may list their streaming heads only, and no list holds streaming heads
 // when none of the CTA's tokens survives in their windows.  A group of D/8
 // lanes keeps to one token; every group of a warp is at the same vector of its
 // own token.
@@ -384,8 +434,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       return;
     }
   }
+  // 8-bit: retrieval heads are listed when no row completes a block; their
+  // tokens then go to the tails (else the scale-block CTAs take them)
+  const bool tails = MODE == kFp8Mode && P.tails_in_rows;
   const int nq = P.q.p ? P.Hq : 0;
-  const int nk_all = MODE == kFp8Mode ? a.n_str : P.Hkv;
+  const int nk_all = MODE == kFp8Mode && !tails ? a.n_str : P.Hkv;
   const int vgroups = (nq + (MODE == kAlone ? 1 : 2) * nk_all + vecs_per_cta - 1) / vecs_per_cta;
   const int cta = (int)blockIdx.x - block_ctas;
   const int64_t tok0 = (int64_t)(cta / vgroups) * kTok;
@@ -407,33 +460,41 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     const int b = a.rows.row[lr];
     const int64_t len = a.rows.len[lr];
     const int64_t p = len + (tok - (int64_t)lr * a.n_tok);
-    kept_ret = MODE != kFp8Mode && a.n_ret > 0 && p >= a.shard_lo && p < a.shard_hi;
+    kept_ret = (MODE != kFp8Mode || tails) && a.n_ret > 0 && p >= a.shard_lo && p < a.shard_hi;
     kept_str = a.n_str > 0 && (p < a.S || p >= len + a.n_tok - a.R);
-    if (kept_ret) {
+    if (kept_ret && MODE == kFp8Mode) {
+      ret0 = (int64_t)b * a.n_ret * kScaleBlock + ((p - a.shard_lo) & (kScaleBlock - 1));
+      ret_step = kScaleBlock;
+    } else if (kept_ret) {
       ret0 = ret_row(a.ret, b, 0, p - a.shard_lo);
       ret_step = a.ret.table ? kPageTokens : a.ret.cap;
     }
     if (kept_str) str0 = (int64_t)b * a.n_str * a.Ws + ring_slot(p, a.S, a.R);
     // (a long chunk's middle: retrieval heads only)
     all_kv = __syncthreads_or(alive && kept_str);
-    if (!all_kv) nk = MODE == kFp8Mode ? 0 : a.n_ret;
+    if (!all_kv) nk = MODE == kFp8Mode && !tails ? 0 : a.n_ret;
   }
   const int vecs = nq + (MODE == kAlone ? nk : 2 * nk);
   const int v0 = (cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
   if (v0 >= v1) return;  // the same in the whole CTA
   auto head_of = [&](int h) {
     if (MODE == kAlone) return h;
-    if (MODE == kFp8Mode) return (int)a.h.str_heads[h];
+    if (MODE == kFp8Mode && !tails) return (int)a.h.str_heads[h];
     return all_kv ? h : (int)a.h.ret_heads[h];
   };
   const bool turn = P.rope.rot_dim > 0 && v0 < nq + nk;
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turn) {
-    fill_angles<D, kTok>(P.rope, s_cos, s_sin, [&](int i) {
-      const int64_t tk = min(tok0 + i, P.tokens - 1);
-      if (MODE == kAlone || P.positions) return P.positions[tk];
-      const int lr = row_of(tk);
-      return (int64_t)a.rows.len[lr] + (tk - (int64_t)lr * a.n_tok);
+    fill_angles<D, kTok>(P.rope, s_cos, s_sin, [&](int i, int64_t &p) {
+      const int64_t tk = tok0 + i;
+      if (tk >= P.tokens) return false;
+      if (MODE == kAlone || P.positions) {
+        p = P.positions[tk];
+      } else {
+        const int lr = row_of(tk);
+        p = (int64_t)a.rows.len[lr] + (tk - (int64_t)lr * a.n_tok);
+      }
+      return true;
     });
     __syncthreads();
     c = *reinterpret_cast<const float4 *>(s_cos + (group % kTok) * (D / 2) + 4 * sl);
@@ -493,9 +554,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   // cache rows of K or V heads
   auto put_kv = [&](bool isv, int h, float (&x)[8], bool ok) {
     const int kvh = head_of(h);
-    const bool ret = MODE != kFp8Mode && a.h.kind[kvh];
+    const bool ret = a.h.kind[kvh];
     const int64_t row = ret ? ret0 + a.h.index[kvh] * ret_step : str0 + (int64_t)a.h.index[kvh] * a.Ws;
-    uint8_t *base = ret ? (isv ? a.p.ret_v : a.p.ret_k) : (isv ? a.p.str_v : a.p.str_k);
+    uint8_t *base = !ret               ? (isv ? a.p.str_v : a.p.str_k)
+                    : MODE == kFp8Mode ? (isv ? P.tail.v : P.tail.k)
+                                       : (isv ? a.p.ret_v : a.p.ret_k);
     if constexpr (MODE == kInt4) {
       uint8_t *szs = ret ? (isv ? a.p.ret_v_sz : a.p.ret_k_sz) : (isv ? a.p.str_v_sz : a.p.str_k_sz);
       // rounded to bf16 first, so that the codes are those of appending the
@@ -533,7 +596,7 @@ template <typename T, int D, int MODE>
 cudaError_t run(const RopeRowsParams &P, int64_t block_ctas, cudaStream_t s) {
   constexpr int SUB = kThreads / (D / 8) / kTok;
   const int nq = P.q.p ? P.Hq : 0;
-  const int nk = MODE == kFp8Mode ? P.a.n_str : P.Hkv;
+  const int nk = MODE == kFp8Mode && !P.tails_in_rows ? P.a.n_str : P.Hkv;
   const int64_t vecs = nq + (MODE == kAlone ? nk : 2 * nk);
   // A CTA takes all its tokens' vectors when there are tokens enough for
   // every SM, so that each angle is formed once; else as few as its lane
@@ -571,20 +634,27 @@ cudaError_t launch_append_rope(const RopeRowsParams &Pin, int kv_type, cudaStrea
   if (kv_type == kBF16) return d128 ? ra::run<bf, 128, ra::kRaw>(P, 0, s) : ra::run<bf, 64, ra::kRaw>(P, 0, s);
   if (kv_type == kINT4) return d128 ? ra::run<bf, 128, ra::kInt4>(P, 0, s) : ra::run<bf, 64, ra::kInt4>(P, 0, s);
   if (kv_type != kFP8 || !d128) return cudaErrorInvalidValue;
-  // 8-bit: per launch row one item per block that becomes full (at least
-  // one), times groups of retrieval heads, K and V apart
-  int64_t items = 0;
+  // 8-bit: per launch row one item per block that becomes full (at least one,
+  // for the tail), times groups of retrieval heads, K and V apart.  A call
+  // that completes no block, such as most decode steps, leaves the tails to
+  // the row CTAs (64 rows x 1 token: 7.7 us with scale-block CTAs, 5.5 so).
+  int64_t items = 0, full = 0;
   for (int r = 0; r < a.rows.n; ++r) {
     const int64_t len = a.rows.len[r];
     const int64_t l0 = std::max<int64_t>(0, std::min<int64_t>(len, a.shard_hi) - a.shard_lo);
     const int64_t l1 = std::max<int64_t>(0, std::min<int64_t>(len + a.n_tok, a.shard_hi) - a.shard_lo);
-    if (l1 > l0) items = std::max<int64_t>(items, std::max<int64_t>(1, (l1 >> kScaleShift) - (l0 >> kScaleShift)));
+    const int64_t blocks = (l1 >> kScaleShift) - (l0 >> kScaleShift);
+    full = std::max(full, blocks);
+    if (l1 > l0) items = std::max(items, std::max<int64_t>(1, blocks));
   }
+  P.tails_in_rows = full == 0;
   int64_t ctas = 0;
   P.block_items = (int)std::max<int64_t>(1, items);
   P.heads_per_cta = 1;
-  if (items > 0 && a.n_ret > 0) {
-    // several heads share a token's angles; one each while that leaves SMs idle
+  if (full > 0 && a.n_ret > 0) {
+    // A CTA's heads share its tokens' angles: as many as leave two CTAs an SM
+    // (8192 tokens, 4 heads, with the queries: 48.5, 44.4 and 42.4 us for 1, 2
+    // and 4 heads a CTA).
     while (P.heads_per_cta < a.n_ret &&
            2 * a.rows.n * items * ((a.n_ret + 2 * P.heads_per_cta - 1) / (2 * P.heads_per_cta)) >= 148 * 2)
       P.heads_per_cta *= 2;
