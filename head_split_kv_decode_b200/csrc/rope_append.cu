@@ -129,16 +129,23 @@ __device__ __forceinline__ uint64_t turn_rate(float inv_freq) {
 __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t rate) {
   const uint32_t t = (uint32_t)(((uint64_t)pos * rate) >> 32);
   const uint32_t q = (t + 0x20000000u) >> 30;  // nearest quarter turn
-  const float x = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const int32_t r = (int32_t)(t - (q << 30));
+  // x + dx = r * 2 pi / 2^32 to twice the precision, so that a key's rounding
+  // does not depend on the angle's
+  constexpr float kUnit = 1.46291807e-9f, kUnitLow = (float)(6.283185307179586 / 4294967296.0 - (double)kUnit);
+  const float rh = (float)(r & ~255), rl = (float)(r & 255);  // both exact
+  const float x = rh * kUnit;
+  const float dx = fmaf(rl, kUnit, fmaf(rh, kUnitLow, fmaf(rh, kUnit, -x)));
   const float z = x * x;
-  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
-  s = fmaf(z, s, 8.3333333e-3f);                     // 1/5!
-  s = fmaf(z, s, -0.16666667f);                      // -1/3!
-  s = fmaf(x * z, s, x);
   float c = fmaf(z, 2.4801587e-5f, -1.3888889e-3f);  // 1/8!, -1/6!
   c = fmaf(z, c, 4.1666667e-2f);                     // 1/4!
-  c = fmaf(z, c, -0.5f);
-  c = fmaf(z, c, 1.f);
+  c = z * fmaf(z, c, -0.5f);                         // cos x - 1
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, -1/7!
+  s = fmaf(z, s, 8.3333333e-3f);                     // 1/5!
+  s = x * z * fmaf(z, s, -0.16666667f);              // sin x - x, -1/3!
+  const float sx = x + s;
+  s = x + fmaf(dx, 1.f + c, s);
+  c = 1.f + fmaf(-dx, sx, c);
   const float a = q & 1 ? s : c, b = q & 1 ? c : s;
   // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
   return make_float2(__uint_as_float(__float_as_uint(a) ^ (((q + 1) & 2) << 30)),
@@ -189,7 +196,12 @@ __device__ __forceinline__ void norm8(float eps, const float (&w)[8], float (&x)
   for (int i = 1; i < 4; ++i)
     s = ffma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(x[2 * i], x[2 * i + 1]), s);
   const float ss = vec_sum<D / 8>(s.x + s.y);
-  const float inv = rsqrtf(ss * (1.f / D) + eps);
+  // one Newton step behind the approximate root, so that a result's rounding
+  // does not depend on it (the correctly rounded root costs 5% of the append)
+  const float var = ss * (1.f / D) + eps;
+  float inv = rsqrtf(var);
+  const float err = fmaf(-var * inv, inv, 1.f);
+  if (fabsf(err) < 0.5f) inv = fmaf(0.5f * inv, err, inv);  // not for 0 and infinity
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = fmul2(fmul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(inv, inv)),

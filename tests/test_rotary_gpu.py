@@ -5,10 +5,9 @@ Tolerance.  The result is rounded once to its type: half a step, 2^-8 (bf16)
 or 2^-24 (fp32) of it.  Before that the kernel works in fp32; relative to
 |y_a| + |y_b| of a channel's pair it is off by at most: the sum of squares
 (8 serial and 4 tree additions on D = 128, halved by the root: 6 units of
-2^-24) + rsqrt (2) + two products (2) + the turn fraction's rounding (2^-25
-turn = 3.2 units) + sine and cosine (2 each; bf16: the hardware's, 2^-20.5) +
-mscale (1) + product and fma (2): under 24 units for fp32, and 24 * 2^-24 +
-2^-20 for bf16.
+2^-24) + the root (2) + two products (2) + the turn fraction (2^-32 turn and
+the fixed-point rate: 1) + sine and cosine (2 each, the Taylor sums' first
+omitted terms among them) + mscale (1) + product and fma (2): under 24 units.
 """
 
 import numpy as np
@@ -45,10 +44,7 @@ def assert_rotated(got, x, pos, rot, weight, eps, inv_freq, interleaved, mscale,
     freq = f64(inv_freq) if rot else np.zeros(0)
     ref = OR.rotate(y, pos, freq, interleaved, mscale) if rot else y
     size = OR.pair_size(y, rot, interleaved, mscale)
-    if got.dtype == BF:
-        tol = 2.0 ** -8 * np.abs(ref) + (24 * 2.0 ** -24 + 2.0 ** -20) * size
-    else:
-        tol = 2.0 ** -24 * np.abs(ref) + 24 * 2.0 ** -24 * size
+    tol = (2.0 ** -8 if got.dtype == BF else 2.0 ** -24) * np.abs(ref) + 24 * 2.0 ** -24 * size
     err = np.abs(f64(got) - ref)
     bad = ~(err <= tol)
     assert not bad.any(), "%s: %d off, worst %.3g of %.3g" % (
