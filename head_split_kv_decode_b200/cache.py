@@ -146,8 +146,9 @@ class DuoCache:
             out = q_out
             if qh is not None and out is None:
                 out = q.new_empty(q_shape)
-            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh, kh, vh, pos_ptr, n,
-                                   None if out is None else out.data_ptr(), handle)
+            with_q = out is not None and n > 0  # (empty tensors have no address)
+            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh if with_q else None, kh, vh,
+                                   pos_ptr, n, out.data_ptr() if with_q else None, handle)
             return out
 
         return run_on(dev, stream, call)

@@ -723,6 +723,7 @@ duo_status decode_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &
                        bool check_next = false) {
   if (!q || !std::isfinite(scale)) return DUO_ERR_ARG;
   if (part ? (!part->o || !part->lse) : !out) return DUO_ERR_ARG;
+  if (is_fp8(c) && !aligned16(q)) return DUO_ERR_ARG;  // read 16 bytes at a time
   const bool fused = k_new != nullptr;
   // A shard's decode is only meaningful as a partial to be merged; partials
   // come from the tensor-core decode and do not append.

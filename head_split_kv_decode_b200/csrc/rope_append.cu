@@ -525,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       load_quad(static_cast<const T *>(wp) + qd.b, w + 4);
     }
     const T *in = static_cast<const T *>(view.p) + tok * view.tok;
-    const int step = (int)view.head;
     auto fetch = [&](Raw<T> &raw, int v) {
       if (MODE != kAlone && kv) {
         const int h = head_of(v);
@@ -534,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
         if (live) raw.load(in + (int64_t)h * view.head, qd.a, qd.b);
         return live;
       }
-      raw.load(in + (int64_t)v * step, qd.a, qd.b);
+      raw.load(in + (int64_t)v * view.head, qd.a, qd.b);
       return alive;
     };
     auto finish = [&](const Raw<T> &raw, int v, bool ok) {

@@ -270,7 +270,8 @@ duo_status duo_qk_norm_rope(const duo_rope_desc *rope, int32_t dtype, int64_t n_
  * row r is token r * n_tokens + i of k, v, q and positions.  positions (device
  * [rows * n_tokens]) gives the rotation's positions, NULL takes each token's
  * place in its row; where a token is stored never depends on it.  q and q_out
- * are given together or are both NULL.  n_tokens == 0 changes nothing.
+ * are given together or are both NULL; q_out may be q in place (dense strides)
+ * and overlaps no other tensor.  n_tokens == 0 changes nothing.
  * Errors: as duo_append_kv, and DUO_ERR_ARG for a bad description or
  * alignment; nothing is enqueued or changed then. */
 duo_status duo_append_rope(duo_cache *cache, int32_t layer, const duo_rope_desc *rope,
@@ -296,7 +297,8 @@ duo_status duo_append_rope_rows(duo_cache *cache, int32_t layer, const int32_t *
  * buffer.  softmax_scale <= 0 means 1/sqrt(d).  The workspace must be
  * zero-filled before its first use with any cache; each call leaves its
  * counters at zero again.  Workspace size: from duo_cache_required_bytes.
- * Errors: DUO_ERR_STATE if a row is empty; DUO_ERR_UNSUPPORTED for rows of
+ * Errors: DUO_ERR_STATE if a row is empty; DUO_ERR_ARG for queries of a
+ * DUO_FP8 cache that are not 16-byte aligned; DUO_ERR_UNSUPPORTED for rows of
  * different lengths on a configuration without the tensor-core decode (fp32
  * caches, head_dim 64). */
 duo_status duo_decode_attn(duo_cache *cache, int32_t layer, const void *q,

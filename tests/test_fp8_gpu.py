@@ -312,6 +312,93 @@ def test_static_scratch_decode(cuda_lib):
         assert torch.equal(out, ref)
 
 
+def test_offsets_past_32_bits(cuda_lib):
+    """Code buffers of 4.9 GB: the last heads and the last batch row lie past 2^32 bytes."""
+    hq = hkv = 64
+    cache = DuoCache(1, 2, hq, hkv, D, "fp8", 300000, torch.ones(1, hkv), 4, 60)
+    cache.set_decode_output(torch.float32)
+    assert cache.region(0, "ret_k").numel() > 1 << 32
+    n = 100
+    k, v, q = _seq(1, n, hkv), _seq(2, n, hkv), _seq(3, 1, hq)
+    cache.append(0, torch.stack([k, k]), torch.stack([v, v]))
+    out = cache.decode(0, torch.cat([q, q]))
+    ref, tol = _reference(q[0], k, v, torch.ones(hkv, dtype=torch.uint8), 4, 60)
+    for b in range(2):
+        assert_close(out[b], ref, tol)
+    cache.close()
+
+
+def test_shard_without_keys(cuda_lib):
+    """A shard that holds no position yet: retrieval partials empty, streaming heads whole."""
+    mask = torch.tensor([1, 0], dtype=torch.uint8)
+    k, v, q = _seq(1, 90, 2), _seq(2, 90, 2), _seq(3, 1, 8)
+    c = DuoCache(1, 1, 8, 2, D, "fp8", 64, mask[None], 4, 60)
+    c.set_retrieval_shard(2000, 1 << 62)
+    c.append(0, k[None], v[None])
+    for own in (True, False):
+        o, lse = c.decode_partial(0, q, owns_streaming=own)
+        torch.cuda.synchronize()
+        assert (o[0, :4] == 0).all() and (lse[0, :4] == -float("inf")).all()
+        assert torch.isfinite(lse[0, 4:]).all() if own else (lse[0, 4:] == -float("inf")).all()
+    ref, tol = _reference(q[0], k, v, torch.zeros(2, dtype=torch.uint8), 4, 60)
+    o, _ = c.decode_partial(0, q)
+    assert_close(o[0, 4:], ref[4:], tol[4:])
+
+
+def test_captured_steps_and_two_caches(cuda_lib):
+    """Append with rotation and decode captured into graphs of two caches that
+    share nothing, replayed at the same time on two streams: each replay writes
+    the same slots and attends to them, whatever its inputs hold by then."""
+    rot = Rotary((10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda(), D)
+    work = []
+    for i in range(2):
+        n = 1000 + 37 * i
+        cache, mask = _cache(1, 8, 2, 1, n + 1, paged=bool(i))
+        k, v = _seq(10 + i, n + 2, 2), _seq(20 + i, n + 2, 2)
+        cache.append(0, k[None, :n], v[None, :n])
+        cache.set_decode_reproducible(True)
+        x = _seq(30 + i, 2, 12).view(2, 1, 1, 12, D)
+        io = x[0].clone()
+        cache.decode(0, io[0, :, :8].contiguous())  # launch facts looked up before the capture
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            q = cache.append_rope(0, rot, io[:, :, 8:10], io[:, :, 10:], q=io[:, :, :8])
+            out = cache.decode(0, q[:, 0])
+        work.append((cache, mask, k[:n], v[:n], x, io, g, s, out, n))
+    for t in (0, 1):
+        for *_, x, io, g, s, out, n in work:
+            io.copy_(x[t])
+        torch.cuda.synchronize()
+        for *_, g, s, out, n in work:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for cache, mask, k, v, x, io, g, s, out, n in work:
+            pos = torch.tensor([[n]], device="cuda")
+            q1, k1 = qk_norm_rope(rot, x[t][:, :, :8], x[t][:, :, 8:10], pos)
+            ref, tol = _reference(q1[0, 0], torch.cat([k, k1[0]]), torch.cat([v, x[t][0, :, 10:]]), mask, 4, 60)
+            assert_close(out[0], ref, tol)
+
+
+def test_side_stream_and_default_stream(cuda_lib):
+    """The same calls on a side stream give the same bits as on the current one."""
+    rot = Rotary((10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda(), D)
+    x = _seq(40, 70, 12).view(1, 70, 12, D)
+    outs = []
+    for side in (None, torch.cuda.Stream()):
+        cache, mask = _cache(1, 8, 2, 1, 100)
+        cache.set_decode_reproducible(True)
+        torch.cuda.synchronize()
+        q = cache.append_rope(0, rot, x[:, :, 8:10], x[:, :, 10:], q=x[:, :, :8], stream=side)
+        if side is not None:
+            side.synchronize()
+        o = cache.decode(0, q[:, -1].contiguous(), stream=side)
+        torch.cuda.synchronize()
+        outs.append((q, o, cache.storage.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 @pytest.mark.parametrize("world", [2, 3])
 def test_sequence_shards(cuda_lib, world):
     """Shards (odd boundaries: blocks count from the shard's first position),
@@ -401,6 +488,13 @@ def test_calls_refused(cuda_lib):
     assert e.value.name == "DUO_ERR_STATE"
     k = _seq(1, 40, 2)
     cache.append(0, k[None], k[None])
+    odd = torch.zeros(8 * D + 1, dtype=BF, device="cuda")[1:].view(1, 8, D)  # contiguous, 2 bytes off
+    with pytest.raises(B.DuoError) as e:
+        cache.decode(0, odd)
+    assert e.value.name == "DUO_ERR_ARG"
+    with pytest.raises(B.DuoError) as e:
+        cache.step(0, odd, k[None, 0], k[None, 0])
+    assert e.value.name == "DUO_ERR_ARG" and cache.seq_len(0) == 40
     with pytest.raises(B.DuoError) as e:  # the 8-bit pre-fill needs its workspace
         B.duo_prefill_attn(cache.handle, 0, q.data_ptr(), k.data_ptr(), k.data_ptr(), 1, q.data_ptr(), 0.0, None, 0)
     assert e.value.name == "DUO_ERR_WORKSPACE"

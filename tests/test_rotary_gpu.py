@@ -222,6 +222,10 @@ def test_append_rope_whole_batch_and_empty(cuda_lib):
     assert q.shape == (2, 5, 4, 128) and cache.seq_len(0) == 5
     before = cache.storage.clone()
     cache.append_rope(0, r, x[:, :0, :2], x[:, :0, 2:])  # nothing
+    none = cache.append_rope(0, r, x[:, :0, :2], x[:, :0, 2:], q=x[:, :0])
+    assert none.shape == (2, 0, 4, 128)
+    a, b = qk_norm_rope(r, x[0, :0], x[0, :0, :2], torch.zeros(0, dtype=torch.int64, device="cuda"))
+    assert a.shape == (0, 4, 128) and b.shape == (0, 2, 128)
     assert cache.seq_len(0) == 5 and torch.equal(before, cache.storage)
 
 
