@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const int nk_all = MODE == kFp8Mode && !tails ? a.n_str : P.Hkv;
   const int vgroups = (nq + (MODE == kAlone ? 1 : 2) * nk_all + vecs_per_cta - 1) / vecs_per_cta;
   const int cta = (int)blockIdx.x - block_ctas;
-  const int64_t tok0 = (int64_t)(cta / vgroups) * kTok;
+  const int64_t tok0 = (int64_t)(vgroups == 1 ? cta : cta / vgroups) * kTok;
   const int group = threadIdx.x / LPR, sl = threadIdx.x % LPR;
   const int sub = group / kTok;
   const bool alive = tok0 + group % kTok < P.tokens;
@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const Quads qd = quads_of(P.rope, sl);
   // launch row of a token (a 64-bit division only where it is needed)
   auto row_of = [&](int64_t tk) {
+    if (a.rows.n == 1) return 0;
     return P.tokens >> 32 ? (int)(tk / a.n_tok) : (int)((uint32_t)tk / (uint32_t)a.n_tok);
   };
   // where the token goes in the cache: rows of its heads, one stride apart
@@ -481,13 +482,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
       ret0 = ret_row(a.ret, b, 0, p - a.shard_lo);
       ret_step = a.ret.table ? kPageTokens : a.ret.cap;
     }
-    if (kept_str) str0 = (int64_t)b * a.n_str * a.Ws + ring_slot(p, a.S, a.R);
+    if (kept_str) {  // (positions and windows fit 31 bits)
+      const uint32_t past = (uint32_t)p - (uint32_t)a.S;
+      str0 = (int64_t)b * a.n_str * a.Ws + (p < a.S ? (uint32_t)p : (uint32_t)a.S + past % (uint32_t)a.R);
+    }
     // (a long chunk's middle: retrieval heads only)
     all_kv = __syncthreads_or(alive && kept_str);
     if (!all_kv) nk = MODE == kFp8Mode && !tails ? 0 : a.n_ret;
   }
   const int vecs = nq + (MODE == kAlone ? nk : 2 * nk);
-  const int v0 = (cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
+  const int v0 = (vgroups == 1 ? 0 : cta % vgroups) * vecs_per_cta, v1 = min(vecs, v0 + vecs_per_cta);
   if (v0 >= v1) return;  // the same in the whole CTA
   auto head_of = [&](int h) {
     if (MODE == kAlone) return h;
