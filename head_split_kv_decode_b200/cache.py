@@ -147,8 +147,12 @@ class DuoCache:
             if qh is not None and out is None:
                 out = q.new_empty(q_shape)
             with_q = out is not None and n > 0  # (empty tensors have no address)
-            B.duo_append_rope_rows(self.handle, layer, rows, desc, qh if with_q else None, kh, vh,
-                                   pos_ptr, n, out.data_ptr() if with_q else None, handle)
+            args = (desc, qh if with_q else None, kh, vh, pos_ptr, n,
+                    out.data_ptr() if with_q else None, handle)
+            if rows is None:
+                B.duo_append_rope(self.handle, layer, *args)
+            else:
+                B.duo_append_rope_rows(self.handle, layer, rows, *args)
             return out
 
         return run_on(dev, stream, call)

@@ -40,8 +40,19 @@ def heads_view(t, shape, name, dtype, device):
         return B.duo_heads(None, 0, 0)
     if st[-1] != 1:
         raise ValueError("%s must have contiguous channels" % name)
+    size = _BYTES[dtype]
+    # the usual forms first: [tokens, heads, d] and [rows, tokens, heads, d]
+    head = st[-2]
+    if len(st) == 3:
+        tok = st[0]
+    elif len(st) == 4 and (shape[1] == 1 or st[0] == st[1] * shape[1]):
+        tok = st[0] if shape[1] == 1 else st[1]
+    else:
+        tok = 1  # not aligned: the general form below
+    if not (ptr | tok * size | head * size) & 15:
+        return B.duo_heads(ptr, tok, head)
     # one stride for all tokens: the innermost leading dimension's, which the
-    # outer ones have to continue
+    # outer ones have to continue; dimensions of size 1 have none
     tok, count = 0, 1
     for i in range(len(shape) - 3, -1, -1):
         if shape[i] == 1:
@@ -51,8 +62,9 @@ def heads_view(t, shape, name, dtype, device):
         elif st[i] != tok * count:
             raise ValueError("%s: its tokens must lie at one stride" % name)
         count *= shape[i]
-    head = st[-2] if shape[-2] > 1 else 0
-    if (ptr | tok * _BYTES[dtype] | head * _BYTES[dtype]) & 15:
+    if shape[-2] == 1:
+        head = 0
+    if (ptr | tok * size | head * size) & 15:
         raise ValueError("%s must start at, and its tokens and heads lie at, multiples of 16 bytes" % name)
     return B.duo_heads(ptr, tok, head)
 

@@ -245,7 +245,11 @@ def test_heads_view_strides():
     assert view(x[:, :, 2:6]) == (1280, 128)
     assert view(x[:, 2:3]) == (6400, 128)              # one token a row: the rows' stride
     assert view(x[:, :, ::2]) == (1280, 256)
-    assert view(x[:1, :, 3:4]) == (1280, 0)
+    assert view(x[:1, :, 3:4]) == (1280, 128)          # (one head: its stride is not used)
+    assert view(x[:1, :1, :, :].expand(1, 1, 10, 128)) == (6400, 128)
+    assert view(x[0]) == (1280, 128) and view(x[0, :1].as_strided((1, 10, 128), (7, 128, 1))) == (0, 128)
+    assert view(x.as_strided((2, 3, 1, 128), (3840, 1280, 5, 1))) == (1280, 0)
+    assert view(x.view(3, 5, 2, 5, 128)[:, :, 0].unsqueeze(1)) == (1280, 128)
     assert view(x.transpose(1, 2)[:1]) == (128, 1280)
     for bad in (x[:, 1:], x[:, ::2], x.transpose(0, 1), x[..., :64].transpose(2, 3),
                 x.flatten()[1:1 + 2 * 1280].view(2, 10, 128)):
