@@ -836,24 +836,49 @@ cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t s) {
   return pf::launch<false>(p, PrefillSplit{}, s);
 }
 
+// End of the launch (us) when `first` CTAs of `t_first` each and then `rest`
+// CTAs of `t_rest` each are handed to sms SMs in this order.
+static double launch_span(int64_t first, double t_first, int64_t rest, double t_rest, int sms) {
+  // SMs that take one CTA of the first kind less than the others, and those
+  int64_t n[2] = {sms - first % sms, first % sms};
+  double at[2] = {(double)(first / sms) * t_first, (double)(first / sms + 1) * t_first};
+  double end = n[1] ? at[1] : at[0];
+  while (rest > 0) {
+    const int g = n[1] && at[1] < at[0] ? 1 : 0;
+    rest -= n[g];
+    at[g] += t_rest;
+    if (at[g] > end) end = at[g];
+  }
+  return end;
+}
+
 // How many runs a retrieval item's tiles are cut into.  Measured: a CTA (one
-// per SM) takes about 2.4 us per tile of its pair of query tiles; the merge
-// costs about 4 us and its partials' bytes.  The fewest waves of the longest
-// run win, if they save a tenth.
+// per SM) takes about 6 us and 2.4 us per tile of its pair of query tiles; the
+// merge costs about 4 us and its partials' bytes.  Taken: the count whose
+// launch, the streaming items behind the retrieval runs, ends first, if it
+// saves a tenth.  (A few CTAs too many for the SMs cost a whole further wave:
+// 16 queries on 15000 tokens, 16 retrieval and 16 streaming query heads take
+// 68 us a call in nine runs and 58 in eight.)
 int prefill_splits(const PrefillParams &p, int num_sms) {
   using namespace pf;
   const int n_pairs = (p.C + 2 * BM - 1) / (2 * BM);
   const int64_t items = (int64_t)p.rows.n * p.n_ret * p.G * n_pairs;
+  const int64_t str_items = (int64_t)p.rows.n * p.n_str * p.G * n_pairs;
   int64_t len = 0;
   for (int r = 0; r < p.rows.n; ++r) len = len > p.rows.len[r] ? len : p.rows.len[r];
-  const int64_t tiles = (len + BN - 1) / BN + (p.C + BN - 1) / BN;
+  auto tiles_of = [](int64_t keys) { return (keys + BN - 1) / BN; };
+  const int64_t chunk = tiles_of(p.C), tiles = tiles_of(len) + chunk;
+  // a streaming item: the window's tiles, and the chunk's in reach of its rows
+  const int64_t reach = 2 + tiles_of(p.R) + 1;
+  const int64_t str_tiles = tiles_of(len < p.W ? len : p.W) + (chunk < reach ? chunk : reach);
   if (items == 0 || num_sms <= 0) return 1;
+  const double t_str = 6.0 + 2.4 * (double)str_tiles;
+  const int rows = p.C < 2 * BM ? p.C : 2 * BM;
   double best = 0.0, whole = 0.0;
   int ns = 1;
   for (int k = 1; k <= tiles && items * k <= kPrefillSplitCtas; ++k) {
-    const int64_t waves = (items * k + num_sms - 1) / num_sms;
-    double t = 2.4 * (double)waves * (double)((tiles + k - 1) / k);
-    if (k > 1) t += 4.0 + (double)(items * k) * (2 * BM * (HD + 1) * 4.0 * 2.0) / 5e6;
+    double t = launch_span(items * k, 6.0 + 2.4 * (double)((tiles + k - 1) / k), str_items, t_str, num_sms);
+    if (k > 1) t += 4.0 + (double)(items * k) * (rows * (HD + 1) * 4.0 * 2.0) / 5e6;
     if (k == 1) whole = best = t;
     else if (t < best && t < 0.9 * whole) best = t, ns = k;
   }
