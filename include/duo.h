@@ -405,7 +405,8 @@ duo_status duo_prefill_attn_rows(duo_cache *cache, int32_t layer, const int32_t 
 
 /* Workspace bytes duo_prefill_attn needs: 0 for a DUO_BF16 cache; for a
  * DUO_INT4 or DUO_FP8 cache the bf16 size of one layer's retrieval storage rows plus its
- * streaming buffers (K and V), for the largest layer. */
+ * streaming buffers (K and V), for the largest layer; for a DUO_FP8 cache also the
+ * float32 partials of a pre-fill whose keys are split over several CTAs (39 MB). */
 duo_status duo_prefill_workspace_bytes(const duo_cache *cache, size_t *bytes);
 
 /* Sequence sharding, for a sequence too long for one GPU's retrieval caches:
