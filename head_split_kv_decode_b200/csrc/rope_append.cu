@@ -51,13 +51,16 @@ constexpr int kBatch = 4;   // vectors a lane group loads at once
 
 // Threads of a CTA.  Four warps: a chunk's CTAs are all on the SMs at once, and
 // the set-up's latency is paid once (4096 tokens x 40 heads, 1024 CTAs: 15.6 us
-// with 128 threads, 17.6 with 256).  A scale block takes 16 half-warps.
+// with 128 threads, 17.6 with 256).  A scale block takes 16 half-warps (3000
+// tokens of 8 heads: 10.2 us, 13.3 in eight with four tokens each).
 constexpr int kBlockThreads = 256, kRowThreads = 128;
 constexpr int threads_of(int mode) { return mode == kFp8Mode ? kBlockThreads : kRowThreads; }
 // CTAs an SM has to hold: 64 registers a thread, 80 for fp32; 72 for the
-// appends (4 x 1777 tokens of 96 vectors: 43.5 us, 45.7 with 64, 47.0 with 80).
+// appends (4 x 1777 tokens of 96 vectors: 43.5 us, 45.7 with 64, 47.0 with 80);
+// 80 for the 8-bit append, whose scale blocks spill with less (3000 tokens of 32
+// heads: 24.6 us, 31 with 64).
 constexpr int ctas_of(int mode, int elt) {
-  return (elt == 4 ? 768 : mode == kRaw || mode == kInt4 ? 896 : 1024) / threads_of(mode);
+  return (elt == 4 || mode == kFp8Mode ? 768 : mode == kRaw || mode == kInt4 ? 896 : 1024) / threads_of(mode);
 }
 
 // A lane's two quads as loaded: what waits in registers for its turn.  Every
@@ -90,6 +93,19 @@ struct Raw<__nv_bfloat16> {
       const float2 f = bf16x2_to_f2(w[i]);
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
+  }
+  __device__ __forceinline__ void pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    a = make_uint2(w[0], w[1]), b = make_uint2(w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p, int qa, int qb) const {
+    *reinterpret_cast<uint2 *>(p + qa) = a;
+    *reinterpret_cast<uint2 *>(p + qb) = b;
   }
 };
 
@@ -300,12 +316,13 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // One scale-block CTA: launch row r, K or V (isv), heads [h0, h1), item `item`
-// (see the launch).  256 threads = 16 half-warps, 2 tokens each.
+// (see the launch).  A half-warp takes NB neighbouring tokens.
 template <bool IL>
 __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool isv, int h0, int h1,
                                           int item, float *s_cos, float *s_sin) {
   using bf = __nv_bfloat16;
   constexpr int D = 128;
+  constexpr int NB = kScaleBlock / (kBlockThreads / 16);  // tokens of a half-warp
   __shared__ float s_max[2][kBlockThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5;
   const int hw = tid >> 4, sl = tid & 15;  // half-warp, lane in the vector
@@ -343,29 +360,24 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
     const int64_t first = blk << kScaleShift;  // local row of the block's first token
     const int64_t t0 = first + a.shard_lo - len;  // its token of the call (negative: older)
     const int64_t tok0 = (int64_t)r * a.n_tok + t0;
-    const bf *src[2];
-    bool fresh[2], have[2];
+    const bf *src = static_cast<const bf *>(in.p) + (tok0 + hw * NB) * in.tok;
+    bool fresh[NB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t l = first + hw * 2 + i;
+    for (int i = 0; i < NB; ++i) {
+      const int64_t l = first + hw * NB + i;
       fresh[i] = l >= l0 && l < l1;
-      have[i] = full || fresh[i];
-      src[i] = static_cast<const bf *>(in.p) + (tok0 + hw * 2 + i) * in.tok;
     }
-    // a head's two vectors of this half-warp; the next head's are loaded
-    // before this one's are exchanged
-    auto fetch = [&](int h, Raw<bf> (&x)[2]) {
-      const int kvh = a.h.ret_heads[h];
-      const bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bf *p = fresh[i] ? src[i] + (int64_t)kvh * in.head : tail + (hw * 2 + i) * D;
-        x[i] = Raw<bf>{};
-        if (have[i]) x[i].load(p, qd.a, qd.b);
-      }
+    // token i of a head: the input's, or an older one from the tail
+    auto fetch = [&](int h, int i, Raw<bf> &x) {
+      x = Raw<bf>{};
+      if (fresh[i])
+        x.load(src + i * in.tok + (int64_t)a.h.ret_heads[h] * in.head, qd.a, qd.b);
+      else if (full)
+        x.load(tails + (((int64_t)b * a.n_ret + h) * kScaleBlock + hw * NB + i) * D, qd.a, qd.b);
     };
-    Raw<bf> raw[2];
-    fetch(h0, raw);
+    Raw<bf> raw[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) fetch(h0, i, raw[i]);
     // (a table entry is read once for all heads; an open block's is not needed)
     const int64_t row0 = full ? ret_row(a.ret, b, 0, first) : 0;
     const int64_t head_step = a.ret.table ? kPageTokens : a.ret.cap;
@@ -379,37 +391,36 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       });
     __syncthreads();
     for (int h = h0; h < h1; ++h) {
-      float mx = 0.f, z[2][8];
+      float mx = 0.f;
+      Raw<bf> z[NB];  // finished: rounded to bf16, what rotated keys are everywhere else
 #pragma unroll
-      for (int i = 0; i < 2; ++i) raw[i].unpack(z[i]);
-      if (h + 1 < h1) fetch(h + 1, raw);
+      for (int i = 0; i < NB; i += 2) {
+        float x[2][8];
+        raw[i].unpack(x[0]);
+        raw[i + 1].unpack(x[1]);
+        z[i] = raw[i], z[i + 1] = raw[i + 1];
+        // the next head's are loaded before this one's are exchanged
+        if (h + 1 < h1) fetch(h + 1, i, raw[i]), fetch(h + 1, i + 1, raw[i + 1]);
+        if (norm) norm8<D>(P.rope.eps, w, x[0], x[1]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float y[8];
+        for (int k = 0; k < 2; ++k) {
+          if (turn) {
+            const int at = (hw * NB + i + k) * (D / 2) + 4 * sl;
+            const float4 c = *reinterpret_cast<const float4 *>(s_cos + at);
+            const float4 s = *reinterpret_cast<const float4 *>(s_sin + at);
+            rotate8<IL>(c, s, x[k]);
+          }
+          if (fresh[i + k]) z[i + k].pack(x[k]);
+          z[i + k].unpack(x[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = z[i][j];
-        if (norm) norm8<D>(P.rope.eps, w, y);
-        if (turn) {
-          const int at = (hw * 2 + i) * (D / 2) + 4 * sl;
-          const float4 c = *reinterpret_cast<const float4 *>(s_cos + at);
-          const float4 s = *reinterpret_cast<const float4 *>(s_sin + at);
-          rotate8<IL>(c, s, y);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // rounded to bf16 first: what the rotated keys are everywhere else
-          if (fresh[i]) z[i][j] = __bfloat162float(__float2bfloat16_rn(y[j]));
-          mx = fmaxf(mx, finite_abs(z[i][j]));
+          for (int j = 0; j < 8; ++j) mx = fmaxf(mx, finite_abs(x[k][j]));
         }
       }
       if (!full) {
-        bf *tail = tails + ((int64_t)b * a.n_ret + h) * kScaleBlock * D;
+        bf *tail = tails + (((int64_t)b * a.n_ret + h) * kScaleBlock + hw * NB) * D;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!fresh[i]) continue;
-          store_quad(tail + (hw * 2 + i) * D + qd.a, z[i]);
-          store_quad(tail + (hw * 2 + i) * D + qd.b, z[i] + 4);
-        }
+        for (int i = 0; i < NB; ++i)
+          if (fresh[i]) z[i].store(tail + i * D, qd.a, qd.b);
         continue;
       }
 #pragma unroll
@@ -424,10 +435,12 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       const float inv = pow2i(-e);
       const int64_t row = row0 + h * head_step;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint8_t *at = codes + (row + hw * 2 + i) * D;
-        *reinterpret_cast<uint32_t *>(at + qd.a) = e4m3x4(z[i], inv);
-        *reinterpret_cast<uint32_t *>(at + qd.b) = e4m3x4(z[i] + 4, inv);
+      for (int i = 0; i < NB; ++i) {
+        float x[8];
+        z[i].unpack(x);
+        uint8_t *at = codes + (row + hw * NB + i) * D;
+        *reinterpret_cast<uint32_t *>(at + qd.a) = e4m3x4(x, inv);
+        *reinterpret_cast<uint32_t *>(at + qd.b) = e4m3x4(x + 4, inv);
       }
       if (tid == 0) scales[row >> kScaleShift] = pow2i(e);
     }
@@ -590,10 +603,10 @@ __global__ void __launch_bounds__(threads_of(MODE), ctas_of(MODE, sizeof(T)))
 #pragma unroll
       for (int i = 0; i < kBatch; i += 2) {
         // two norms at once where the registers allow (4096 tokens x 40 heads:
-        // 14.4 us, 15.6 one by one; the appends would spill: 48.4 against 43.5)
+        // 14.4 us, 15.6 one by one; the other appends: 48.4 against 43.5)
         float x[8], y[8];
         raw[i].unpack(x);
-        if constexpr (MODE == kAlone) {
+        if constexpr (MODE == kAlone || MODE == kFp8Mode) {
           raw[i + 1].unpack(y);
           if (wp) norm8<D>(P.rope.eps, w, x, y);
           finish(x, v + i * SUB, ok[i]);
