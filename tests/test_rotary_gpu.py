@@ -144,6 +144,28 @@ def test_special_values_stay_in_their_vector(cuda_lib):
     assert a[2, 1].isnan().all() and (b[4, 1] == 0).all()
 
 
+@pytest.mark.parametrize("dt,d,rot,il", [(BF, 128, 32, False), (BF, 128, 48, True), (F32, 64, 16, True),
+                                         (F32, 128, 112, False), (BF, 64, 48, False)])
+def test_channels_past_rot_dim_keep_their_bits(cuda_lib, dt, d, rot, il):
+    """Infinities, NaN and negative zeros there neither change nor reach another channel."""
+    n = 9
+    x = _tokens(17, n, 3, d, dt)
+    special = torch.tensor([float("inf"), float("-inf"), float("nan"), -0.0], device="cuda", dtype=dt)
+    x[:, :, rot:] = torch.where(torch.arange(d - rot, device="cuda") % 3 == 0, x[:, :, rot:],
+                                special[torch.arange(d - rot, device="cuda") % 4])
+    pos = torch.arange(n, device="cuda") + 11
+    freq = _inv_freq(rot)
+    r = Rotary(freq, d, interleaved=il)
+    o, _ = qk_norm_rope(r, x, None, pos)
+    got, want, bits = o[..., rot:].contiguous(), x[..., rot:].contiguous(), torch.int16 if dt == BF else torch.int32
+    assert torch.equal(got.isnan(), want.isnan())  # (a NaN's payload is not kept)
+    assert torch.equal(got.view(bits)[~want.isnan()], want.view(bits)[~want.isnan()])
+    clean = x.clone()
+    clean[:, :, rot:] = 0
+    want, _ = qk_norm_rope(r, clean, None, pos)
+    assert torch.equal(o[..., :rot], want[..., :rot])
+
+
 def test_graph_capture_and_replay(cuda_lib):
     n, d = 9, 128
     q, k = _tokens(10, n, 8, d, BF), _tokens(11, n, 2, d, BF)
