@@ -35,7 +35,9 @@
 // 2^e (finite values), code = x / scale rounded to nearest even e4m3,
 // saturating (an infinity takes the largest code, a NaN stays one).  A power
 // of two makes the division and the expansion to bf16 exact.  8192 tokens of 4
-// retrieval heads with 32 query heads: 43 us (0.56), 17.5 of them the blocks'.
+// retrieval heads with 32 query heads: 43 us (0.57); without queries 16.7, most
+// of it the blocks: an angle is formed for four heads only, and each CTA's
+// set-up, loads, largest values and stores follow one another.
 #include <algorithm>
 
 #include "common.cuh"
@@ -48,17 +50,21 @@ enum Mode : int { kAlone = 0, kRaw = 1, kInt4 = 2, kFp8Mode = 3 };
 
 constexpr int kTok = 4;     // tokens of a row CTA
 constexpr int kBatch = 4;   // vectors a lane group loads at once
+// Heads a scale-block CTA has on their way, asynchronous copies into shared
+// memory (8192 tokens of 32 heads: 38.9 us, three 39.4, loads into registers a
+// head ahead 42.2).
+constexpr int kRing = 2;
 
 // Threads of a CTA.  Four warps: a chunk's CTAs are all on the SMs at once, and
 // the set-up's latency is paid once (4096 tokens x 40 heads, 1024 CTAs: 15.6 us
 // with 128 threads, 17.6 with 256).  A scale block takes 16 half-warps (3000
-// tokens of 8 heads: 10.2 us, 13.3 in eight with four tokens each).
+// tokens of 8 heads: 10 us, 13 in eight with four tokens each).
 constexpr int kBlockThreads = 256, kRowThreads = 128;
 constexpr int threads_of(int mode) { return mode == kFp8Mode ? kBlockThreads : kRowThreads; }
 // CTAs an SM has to hold: 64 registers a thread, 80 for fp32; 72 for the
 // appends (4 x 1777 tokens of 96 vectors: 43.5 us, 45.7 with 64, 47.0 with 80);
 // 80 for the 8-bit append, whose scale blocks spill with less (3000 tokens of 32
-// heads: 24.6 us, 31 with 64).
+// heads: 22.4 us, 28.5 with 64).
 constexpr int ctas_of(int mode, int elt) {
   return (elt == 4 || mode == kFp8Mode ? 768 : mode == kRaw || mode == kInt4 ? 896 : 1024) / threads_of(mode);
 }
@@ -323,6 +329,13 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;  // infinities and NaN do not set the scale
 }
 
+// Eight bytes into shared memory, or zeros (bytes 0: nothing is read).
+__device__ __forceinline__ void cp_async8(void *to, const void *from, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(bytes)
+               : "memory");
+}
+
 // One scale-block CTA: launch row r, K or V (isv), heads [h0, h1), item `item`
 // (see the launch).  A half-warp takes NB neighbouring tokens.
 template <bool IL, bool PART>
@@ -332,6 +345,8 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
   constexpr int D = 128;
   constexpr int NB = kScaleBlock / (kBlockThreads / 16);  // tokens of a half-warp
   __shared__ float s_max[2][kBlockThreads / 32];
+  // heads on their way, each thread's own quads
+  __shared__ __align__(16) uint2 s_ring[kRing][NB][2][kBlockThreads];
   const int tid = threadIdx.x, warp = tid >> 5;
   const int hw = tid >> 4, sl = tid & 15;  // half-warp, lane in the vector
   const AppendParams &a = P.a;
@@ -375,17 +390,25 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       const int64_t l = first + hw * NB + i;
       fresh[i] = l >= l0 && l < l1;
     }
-    // token i of a head: the input's, or an older one from the tail
-    auto fetch = [&](int h, int i, Raw<bf> &x) {
-      x = Raw<bf>{};
-      if (fresh[i])
-        x.load(src + i * in.tok + (int64_t)a.h.ret_heads[h] * in.head, qd.a, qd.b);
-      else if (full)
-        x.load(tails + (((int64_t)b * a.n_ret + h) * kScaleBlock + hw * NB + i) * D, qd.a, qd.b);
-    };
-    Raw<bf> raw[NB];
+    // head h into its slot: the input's tokens, older ones from the tail,
+    // zeros where the open block has neither
+    auto fetch = [&](int h) {
+      if (h < h1) {
+        const bf *in_h = src + (int64_t)a.h.ret_heads[h] * in.head;
+        const bf *tail = tails + (((int64_t)b * a.n_ret + h) * kScaleBlock + hw * NB) * D;
+        const int slot = (h - h0) % kRing;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) fetch(h0, i, raw[i]);
+        for (int i = 0; i < NB; ++i) {
+          const bf *from = fresh[i] ? in_h + i * in.tok : tail + i * D;
+          const int bytes = fresh[i] || full ? 8 : 0;
+          cp_async8(&s_ring[slot][i][0][tid], from + qd.a, bytes);
+          cp_async8(&s_ring[slot][i][1][tid], from + qd.b, bytes);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) fetch(h0 + i);
     // (a table entry is read once for all heads; an open block's is not needed)
     const int64_t row0 = full ? ret_row(a.ret, b, 0, first) : 0;
     const int64_t head_step = a.ret.table ? kPageTokens : a.ret.cap;
@@ -401,14 +424,15 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
     for (int h = h0; h < h1; ++h) {
       float mx = 0.f;
       Raw<bf> z[NB];  // finished: rounded to bf16, what rotated keys are everywhere else
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      const int slot = (h - h0) % kRing;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) z[i].a = s_ring[slot][i][0][tid], z[i].b = s_ring[slot][i][1][tid];
 #pragma unroll
       for (int i = 0; i < NB; i += 2) {
         float x[2][8];
-        raw[i].unpack(x[0]);
-        raw[i + 1].unpack(x[1]);
-        z[i] = raw[i], z[i + 1] = raw[i + 1];
-        // the next head's are loaded before this one's are exchanged
-        if (h + 1 < h1) fetch(h + 1, i, raw[i]), fetch(h + 1, i + 1, raw[i + 1]);
+        z[i].unpack(x[0]);
+        z[i + 1].unpack(x[1]);
         if (norm) norm8<D>(P.rope.eps, w, x[0], x[1]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -429,6 +453,7 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
 #pragma unroll
         for (int i = 0; i < NB; ++i)
           if (fresh[i]) z[i].store(tail + i * D, qd.a, qd.b);
+        fetch(h + kRing);
         continue;
       }
 #pragma unroll
@@ -436,6 +461,7 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       // two sets of slots in turn: one barrier a head
       if ((tid & 31) == 0) s_max[buf][warp] = mx;
       __syncthreads();
+      fetch(h + kRing);  // (the slot's values have been used)
 #pragma unroll
       for (int i = 0; i < kBlockThreads / 32; ++i) mx = fmaxf(mx, s_max[buf][i]);
       buf ^= 1;
