@@ -257,11 +257,12 @@ __device__ __forceinline__ float inv_rms(float ss, float eps) {
   return fabsf(err) < 0.5f ? fmaf(0.5f * inv, err, inv) : inv;  // not for 0 and infinity
 }
 
+// (The weight first: a bf16 value's product with a bf16 weight is exact.)
 __device__ __forceinline__ void scale8(float inv, const float (&w)[8], float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 y = fmul2(fmul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(inv, inv)),
-                           make_float2(w[2 * i], w[2 * i + 1]));
+    const float2 y = fmul2(fmul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(w[2 * i], w[2 * i + 1])),
+                           make_float2(inv, inv));
     x[2 * i] = y.x, x[2 * i + 1] = y.y;
   }
 }
