@@ -677,7 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < HD / 4; ++i)
             dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-          X.lse[at] = l > 0.f ? m + fast_log2(l) : -INFINITY;
+          // -inf marks a run that saw no key (l is 0 then and only then); a
+          // NaN among the scores leaves NaN here, which the merge passes on
+          X.lse[at] = l == 0.f ? -INFINITY : m + fast_log2(l);
         }
       } else if (crow < P.C) {
         uint4 *dst = reinterpret_cast<uint4 *>(out);
@@ -769,7 +771,7 @@ __global__ void prefill_merge_kernel(const __grid_constant__ PrefillParams P,
     acc.x = fmaf(g, v.x, acc.x), acc.y = fmaf(g, v.y, acc.y);
     acc.z = fmaf(g, v.z, acc.z), acc.w = fmaf(g, v.w, acc.w);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   const int rr = r % ret_q;
   const int hq = P.h.ret_heads[rr / P.G] * P.G + rr % P.G;
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
