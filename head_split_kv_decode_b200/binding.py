@@ -123,6 +123,9 @@ SIGNATURES = {
     "duo_set_decode_reproducible": (_I32, [_P, _I32]),
     "duo_set_decode_output": (_I32, [_P, _I32]),
     "duo_test_stall_next_prefill": (_I32, [_P, _I64]),
+    "duo_test_plan_prefill": (_I32, [_P, _I32, ctypes.POINTER(_I32), _I32, _I32, _I32,
+                                     ctypes.POINTER(_I32)]),
+    "duo_test_force_prefill_runs": (_I32, [_P, _I32]),
     "duo_test_plan_decode": (_I32, [_P, _I32, ctypes.POINTER(_I32), _I32, _I32, _I32,
                                     ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
     "duo_decode_splits": (_I32, [_P, _I32, ctypes.POINTER(_I32)]),
@@ -374,6 +377,22 @@ def duo_test_plan_decode(handle, layer, lens, num_sms, ctas_per_sm=1):
     _check(lib().duo_test_plan_decode(handle, layer, arr, n, num_sms, ctas_per_sm, out,
                                       ctypes.byref(pack)), "duo_test_plan_decode")
     return list(out)[:n], pack.value
+
+
+def duo_test_plan_prefill(handle, layer, lens, n_tokens, num_sms):
+    """Testing hook: the runs into which a pre-fill of n_tokens on rows of these
+    lengths cuts each retrieval item's keys on num_sms SMs, computed on the host."""
+    n = len(lens)
+    arr = (_I32 * max(n, 1))(*[int(x) for x in lens])
+    runs = _I32()
+    _check(lib().duo_test_plan_prefill(handle, layer, arr, n, n_tokens, num_sms, ctypes.byref(runs)),
+           "duo_test_plan_prefill")
+    return runs.value
+
+
+def duo_test_force_prefill_runs(handle, runs):
+    """Testing hook: an 8-bit cache's pre-fills take this many runs (0: the planner's choice)."""
+    _check(lib().duo_test_force_prefill_runs(handle, int(runs)), "duo_test_force_prefill_runs")
 
 
 def duo_set_decode_output(handle, dtype):

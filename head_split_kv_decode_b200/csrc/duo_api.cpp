@@ -73,6 +73,7 @@ struct duo_cache {
   bool reproducible;       // decode splits take fixed key shares only
   int32_t out_dtype;       // decode output element type (DUO_F32 or DUO_BF16)
   int64_t stall_ns;        // testing hook: the next pre-fill loads nothing, waits this long
+  int forced_runs;         // testing hook: runs of a split pre-fill, 0 = chosen per launch
   bool have_cfg;           // decode launch facts, queried once per cache
   duo::DecodeConfig cfg;
 };
@@ -439,6 +440,7 @@ duo_status create(duo_cache **out, const duo_cache_desc *desc, const uint8_t *he
   c->reproducible = false;
   c->out_dtype = desc->kv_dtype == DUO_F32 ? DUO_F32 : DUO_BF16;
   c->stall_ns = 0;
+  c->forced_runs = 0;
   c->have_cfg = false;
   c->row_bytes = d.kv_dtype == DUO_INT4 ? d.head_dim / 2 : d.head_dim * elem_bytes(d.kv_dtype);
   c->str_row_bytes = c->row_bytes;
@@ -870,6 +872,26 @@ size_t prefill_ws_bytes(const duo_cache *c) {
   return (size_t)m;
 }
 
+// Fields of a pre-fill launch that are the layer's.
+void fill_prefill_common(const duo_cache *c, int32_t layer, int32_t C, duo::PrefillParams *p) {
+  const auto &L = c->layers[layer];
+  const duo_cache_desc &d = c->desc;
+  p->h = L.h;
+  p->ret = ret_map(c, layer);
+  p->B = d.batch;
+  p->Hq = d.n_q_heads;
+  p->Hkv = d.n_kv_heads;
+  p->G = d.n_q_heads / d.n_kv_heads;
+  p->D = d.head_dim;
+  p->n_ret = L.n_ret;
+  p->n_str = L.n_str;
+  p->S = c->S;
+  p->R = c->R;
+  p->W = c->W;
+  p->C = C;
+  p->retrieval_rows = L.ret_rows;
+}
+
 duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> &rows,
                         const void *q, const void *k, const void *v, int32_t C, void *out,
                         float scale, void *ws, size_t ws_bytes, cudaStream_t s) {
@@ -919,20 +941,7 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
       p.p.str_v = wsb + ps.str_v;
     }
   }
-  p.h = L.h;
-  p.ret = ret_map(c, layer);
-  p.B = d.batch;
-  p.Hq = d.n_q_heads;
-  p.Hkv = d.n_kv_heads;
-  p.G = d.n_q_heads / d.n_kv_heads;
-  p.D = d.head_dim;
-  p.n_ret = L.n_ret;
-  p.n_str = L.n_str;
-  p.S = c->S;
-  p.R = c->R;
-  p.W = c->W;
-  p.C = C;
-  p.retrieval_rows = L.ret_rows;
+  fill_prefill_common(c, layer, C, &p);
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt((float)d.head_dim);
   p.scale_log2 = sc * 1.4426950408889634f;
   p.err = duo::device_error_word();
@@ -962,7 +971,7 @@ duo_status prefill_rows(duo_cache *c, int32_t layer, const std::vector<int32_t> 
                     : duo::launch_dequant_history(dq, s);
       if ((st = cuda_status(e)) != DUO_OK) return st;
     }
-    const int ns = is_fp8(c) ? duo::prefill_splits(p, cfg.num_sms) : 1;
+    const int ns = is_fp8(c) ? duo::prefill_splits(p, cfg.num_sms, c->forced_runs) : 1;
     const cudaError_t e = ns > 1 ? duo::launch_prefill_split(p, ns, split_ws, s) : duo::launch_prefill(p, s);
     if ((st = launch_status(e)) != DUO_OK) return st;
   }
@@ -1405,6 +1414,30 @@ duo_status duo_test_plan_decode(const duo_cache *c, int32_t layer, const int32_t
   }
   *pack = plan_launch(c, layer, rlen, len, n_rows, cfg, ns);
   for (int r = 0; r < n_rows; ++r) splits[r] = ns[r];
+  return DUO_OK;
+}
+
+duo_status duo_test_plan_prefill(const duo_cache *c, int32_t layer, const int32_t *lens,
+                                 int32_t n_rows, int32_t C, int32_t num_sms, int32_t *runs) {
+  if (!c || !lens || !runs || layer < 0 || layer >= c->desc.layers || n_rows <= 0 ||
+      n_rows > duo::kMaxLaunchRows || C <= 0 || num_sms <= 0)
+    return DUO_ERR_ARG;
+  if (c->desc.head_dim != 128 || c->desc.kv_dtype == DUO_F32) return DUO_ERR_UNSUPPORTED;
+  duo::PrefillParams p{};
+  fill_prefill_common(c, layer, C, &p);
+  p.rows.n = n_rows;
+  for (int r = 0; r < n_rows; ++r) {
+    if (lens[r] < 0) return DUO_ERR_ARG;
+    p.rows.len[r] = lens[r];
+  }
+  *runs = is_fp8(c) ? duo::prefill_splits(p, num_sms, c->forced_runs) : 1;
+  return DUO_OK;
+}
+
+duo_status duo_test_force_prefill_runs(duo_cache *c, int32_t runs) {
+  if (!c || runs < 0 || runs > duo::kPrefillSplitCtas) return DUO_ERR_ARG;
+  if (!is_fp8(c)) return DUO_ERR_UNSUPPORTED;
+  c->forced_runs = runs;
   return DUO_OK;
 }
 

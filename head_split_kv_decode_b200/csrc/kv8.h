@@ -79,7 +79,7 @@ cudaError_t launch_decode_fp8(const DecodeFp8Params &p, cudaStream_t s);
 // Keys a CTA of the 8-bit decode walks per iteration; host only.
 int decode_fp8_tile_rows();
 
-int prefill_splits(const PrefillParams &p, int num_sms);  // 1: do not split
+int prefill_splits(const PrefillParams &p, int num_sms, int forced);  // 1: do not split; forced 0: choose
 size_t prefill_split_bytes();
 cudaError_t launch_prefill_split(const PrefillParams &p, int ns, void *ws, cudaStream_t s);
 

@@ -860,8 +860,9 @@ static double launch_span(int64_t first, double t_first, int64_t rest, double t_
 // launch, the streaming items behind the retrieval runs, ends first, if it
 // saves a tenth.  (A few CTAs too many for the SMs cost a whole further wave:
 // 16 queries on 15000 tokens, 16 retrieval and 16 streaming query heads take
-// 68 us a call in nine runs and 58 in eight.)
-int prefill_splits(const PrefillParams &p, int num_sms) {
+// 68 us a call in nine runs and 58 in eight.)  A forced count is taken as far
+// as the workspace holds its partials.
+int prefill_splits(const PrefillParams &p, int num_sms, int forced) {
   using namespace pf;
   const int n_pairs = (p.C + 2 * BM - 1) / (2 * BM);
   const int64_t items = (int64_t)p.rows.n * p.n_ret * p.G * n_pairs;
@@ -874,6 +875,10 @@ int prefill_splits(const PrefillParams &p, int num_sms) {
   const int64_t reach = 2 + tiles_of(p.R) + 1;
   const int64_t str_tiles = tiles_of(len < p.W ? len : p.W) + (chunk < reach ? chunk : reach);
   if (items == 0 || num_sms <= 0) return 1;
+  if (forced > 0) {
+    const int64_t most = kPrefillSplitCtas / items;
+    return most < 1 ? 1 : (int)(forced < most ? forced : most);
+  }
   const double t_str = 6.0 + 2.4 * (double)str_tiles;
   const int rows = p.C < 2 * BM ? p.C : 2 * BM;
   double best = 0.0, whole = 0.0;

@@ -551,6 +551,24 @@ duo_status duo_test_plan_decode(const duo_cache *cache, int32_t layer,
                                 int32_t num_sms, int32_t ctas_per_sm,
                                 int32_t *splits, int32_t *pack);
 
+/* Testing hook for the pre-fill's planner (a scheduling choice; the pages have
+ * no counterpart), host only: no device is touched.  For one launch of n_rows
+ * rows (1 .. DUO_MAX_LAUNCH_ROWS) of this layer with lens[r] >= 0 tokens in
+ * the cache and C in the chunk, on a device of num_sms SMs: the runs into
+ * which each retrieval item's keys are cut (1: not cut, as for every cache
+ * but DUO_FP8).  Errors: DUO_ERR_ARG; DUO_ERR_UNSUPPORTED for a configuration
+ * without pre-fill. */
+duo_status duo_test_plan_prefill(const duo_cache *cache, int32_t layer,
+                                 const int32_t *lens, int32_t n_rows, int32_t C,
+                                 int32_t num_sms, int32_t *runs);
+
+/* Testing hook: a DUO_FP8 cache's pre-fills cut each retrieval item's keys
+ * into this many runs (1 .. 296; fewer where the workspace does not hold
+ * their partials), 0: the planner's choice.  More runs than an item has key
+ * tiles leave some empty.  Errors: DUO_ERR_ARG; DUO_ERR_UNSUPPORTED for other
+ * caches. */
+duo_status duo_test_force_prefill_runs(duo_cache *cache, int32_t runs);
+
 /* Read and clear the device-side error word that bounded in-kernel waits set
  * when they give up.  Synchronises the device.  Returns DUO_ERR_TIMEOUT if it
  * was set, DUO_OK otherwise; *code (may be NULL) receives the raw word.
