@@ -257,15 +257,12 @@ template <typename T, int D, int G>
 static cudaError_t run(const DecodeParams &d, cudaStream_t s, DecodeConfig *cfg) {
   using Sh = DecodeShape<T, D>;
   auto kern = decode_kernel<T, D, G>;
-  static bool attr_done = false;
-  if (!attr_done) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
-    if (e != cudaSuccess) return e;
-    attr_done = true;
-  }
+  static bool smem_done[kMaxDevices] = {};
+  cudaError_t e = allow_dynamic_smem(kern, Sh::kSmem, smem_done);
+  if (e != cudaSuccess) return e;
   if (cfg) {
     int occ = 0, dev = 0, sms = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 128, Sh::kSmem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 128, Sh::kSmem);
     if (e != cudaSuccess) return e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;

@@ -554,19 +554,14 @@ cudaError_t run(const DecodeFp8Params &p, cudaStream_t s, DecodeConfig *cfg) {
   auto kern = decode_fp8_kernel<G>;
   const DecodeParams &d = p.d;
   const int smem = (int)sizeof(float) * (NWARPS * G * D + 2 * NWARPS * G);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static bool smem_done[kMaxDevices] = {};
+  cudaError_t e = allow_dynamic_smem(kern, smem, smem_done);
   if (e != cudaSuccess) return e;
-  static bool attr_done[kMaxDevices] = {};
-  if (dev >= kMaxDevices || !attr_done[dev]) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-      return e;
-    if (dev < kMaxDevices) attr_done[dev] = true;
-  }
   if (cfg) {
-    int occ = 0, sms = 0;
+    int occ = 0, dev = 0, sms = 0;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, NWARPS * 32, smem)) != cudaSuccess)
       return e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     cfg->tile_rows = decode_fp8_tile_rows();
     cfg->ctas_per_sm = occ;

@@ -301,15 +301,12 @@ template <int D, int G>
 static cudaError_t run_int4(const DecodeParams &d, cudaStream_t s, DecodeConfig *cfg) {
   using Sh = Int4Shape<D>;
   auto kern = decode_int4_kernel<D, G>;
-  static bool attr_done = false;
-  if (!attr_done) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
-    if (e != cudaSuccess) return e;
-    attr_done = true;
-  }
+  static bool smem_done[kMaxDevices] = {};
+  cudaError_t e = allow_dynamic_smem(kern, Sh::kSmem, smem_done);
+  if (e != cudaSuccess) return e;
   if (cfg) {
     int occ = 0, dev = 0, sms = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 128, Sh::kSmem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 128, Sh::kSmem);
     if (e != cudaSuccess) return e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;

@@ -173,6 +173,21 @@ struct TableWrites {
   int32_t block[kMaxTableWrites];
 };
 
+// Lets `kern` take `bytes` of dynamic shared memory on the current device: the
+// attribute belongs to a device, so it is set once on each that launches the
+// kernel (`done`: one flag per device, of this kernel).
+template <typename K>
+cudaError_t allow_dynamic_smem(K *kern, int bytes, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev] = true;
+  return e;
+}
+
 // Launch configuration facts the host needs to size splits and workspaces.
 struct DecodeConfig {
   int tile_rows;        // rows per pipeline tile

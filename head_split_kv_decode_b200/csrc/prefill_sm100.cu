@@ -810,22 +810,22 @@ static cudaError_t launch(const PrefillParams &p, const PrefillSplit &x, cudaStr
     ok = make_map(&maps.ks, p.p.str_k, p.W, (uint64_t)p.B * p.n_str, row, row * p.W, BN, 1) &&
          make_map(&maps.vs, p.p.str_v, p.W, (uint64_t)p.B * p.n_str, row, row * p.W, BN, 1);
   if (!ok) return cudaErrorInvalidValue;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<SPLIT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
+  static bool smem_done[kMaxDevices] = {};
+  cudaError_t e = allow_dynamic_smem(prefill_kernel<SPLIT>, kSmemBytes, smem_done);
+  if (e != cudaSuccess) return e;
+  static bool regs_checked = false;
+  if (!regs_checked) {
     // The register split must fit the registers the CTA is launched with, or
     // setmaxnreg.inc would wait for registers that never come.
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, prefill_kernel<SPLIT>)) != cudaSuccess) return e;
     if (128 * (2 * kRegsHigh + kRegsLow) > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
-    attr = true;
+    regs_checked = true;
   }
   const int n_pairs = (p.C + 2 * BM - 1) / (2 * BM);
   const int grid = p.rows.n * (p.n_ret * (SPLIT ? x.ns : 1) + p.n_str) * p.G * n_pairs;
   prefill_kernel<SPLIT><<<grid, kThreads, kSmemBytes, s>>>(p, maps, x);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (!SPLIT || e != cudaSuccess) return e;
   const int64_t warps = (int64_t)p.rows.n * p.n_ret * p.G * p.C;
   prefill_merge_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(p, x);
