@@ -111,7 +111,12 @@ __device__ __forceinline__ void decode_reduce_store(const DecodeParams &P, uint8
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
       const float Mn = fmaxf(M, m);
-      if (Mn == -INFINITY) continue;  // no split of this chunk (or before) saw a key
+      // no split of this chunk (or before) saw a key; a split whose scores were
+      // all NaN has a NaN here, which the maximum leaves out and the sums keep
+      bool none = Mn == -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kHeld / 32; ++i) none = none && x[i] == -INFINITY;
+      if (__all_sync(0xffffffffu, none)) continue;
       const float a = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
       acc *= a;
       den *= a;

@@ -10,7 +10,7 @@ import torch
 
 from head_split_kv_decode_b200 import binding as B
 from head_split_kv_decode_b200 import synth
-from head_split_kv_decode_b200.cache import DuoCache
+from head_split_kv_decode_b200.cache import DuoCache, merge_partials
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,37 @@ def test_split_prefill_keeps_nan(cuda_lib, n, C, bad):
     out = _prefill(n, C, k2, v, q)
     assert out[at:, :4].isnan().all()
     assert torch.equal(out[:at], clean[:at]) and torch.equal(out[:, 4:], clean[:, 4:])
+
+
+# ------------------------------------------------------------------ decode
+
+
+@pytest.mark.parametrize("kv", ["fp8", "bf16", "int4"])
+@pytest.mark.parametrize("splits", [1, 3, 100])
+def test_decode_partials_keep_nan(cuda_lib, kv, splits):
+    """A NaN query makes every score of its head NaN: so are its decode, its
+    share of a sequence shard, and what the shares merge to."""
+    n = 6000
+    mask = torch.tensor([[1, 0]])
+    k, v, q = _seq(1, n, 2), _seq(2, n, 2), _seq(3, 1, 8)
+    q[0, 2, 40] = q[0, 6, 0] = NAN
+    live = [h for h in range(8) if h not in (2, 6)]
+    parts = []
+    for lo, hi in ((0, 2500), (2500, 1 << 62)):
+        c = DuoCache(1, 1, 8, 2, D, kv, n, mask, 4, 60)
+        c.set_retrieval_shard(lo, hi)
+        c.set_decode_splits(splits)
+        c.append(0, k[None], v[None])
+        o, lse = c.decode_partial(0, q, owns_streaming=lo == 0)
+        assert o[0, 2].isnan().all() and lse[0, 2].isnan()
+        if lo == 0:
+            assert o[0, 6].isnan().all() and lse[0, 6].isnan()
+        assert torch.isfinite(o[0, live]).all()
+        parts.append((o, lse))
+    out = merge_partials(torch.stack([p[0] for p in parts]), torch.stack([p[1] for p in parts]),
+                         torch.empty(1, 8, D, device="cuda"))
+    c = DuoCache(1, 1, 8, 2, D, kv, n, mask, 4, 60)
+    c.append(0, k[None], v[None])
+    c.set_decode_splits(splits)
+    for got in (out, c.decode(0, q).float()):
+        assert got[0, (2, 6)].isnan().all() and torch.isfinite(got[0, live]).all()
