@@ -33,7 +33,9 @@
 // its older tokens read from the bf16 tail; tokens of a block that stays open
 // go to the tail.  scale = 2^e, the smallest e >= -120 with max|x| <= 448 *
 // 2^e (finite values), code = x / scale rounded to nearest even e4m3,
-// saturating (an infinity takes the largest code, a NaN stays one).  A power
+// saturating (an infinity takes the largest code, a NaN stays one; at e = 120,
+// where codes past 240 would stand for more than fp32 holds, 240 is the
+// largest).  A power
 // of two makes the division and the expansion to bf16 exact.  8192 tokens of 4
 // retrieval heads with 32 query heads: 43 us (0.57); without queries 16.7, most
 // of it the blocks: an angle is formed for four heads only, and each CTA's
@@ -315,6 +317,18 @@ __device__ __forceinline__ int scale_exp(float amax) {
   return max(e, -120);
 }
 
+// Codes 256 .. 448 at the largest exponent would stand for 2^128 and more,
+// which neither fp32 nor bf16 holds: there values past code 240's take that
+// code (bf16's largest is off by 6%, not infinite when it is read).  A NaN
+// compares false and stays.
+constexpr int kTopExp = 120;
+__device__ __forceinline__ void cap_top(float (&x)[8]) {
+  constexpr float kTop = 240.f * 1.329227995784916e36f;  // 240 * 2^120
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (fabsf(x[j]) > kTop) x[j] = copysignf(kTop, x[j]);
+}
+
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
 // Four codes of x * inv, first in the low byte.
@@ -473,6 +487,7 @@ __device__ __forceinline__ void block_cta(const RopeRowsParams &P, int r, bool i
       for (int i = 0; i < NB; ++i) {
         float x[8];
         z[i].unpack(x);
+        if (e == kTopExp) cap_top(x);
         uint8_t *at = codes + (row + hw * NB + i) * D;
         *reinterpret_cast<uint32_t *>(at + qd.a) = e4m3x4(x, inv);
         *reinterpret_cast<uint32_t *>(at + qd.b) = e4m3x4(x + 4, inv);

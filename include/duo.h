@@ -95,7 +95,8 @@ typedef enum duo_status {
  * its first position) has scale 2^e, the smallest e >= -120 with
  * max|x| <= 448 * 2^e over its finite values, and code x / 2^e rounded to the
  * nearest e4m3 (ties to even; an infinity takes the largest code, a NaN stays
- * one).  A block is coded when it is full; until then its tokens stay in bf16
+ * one; at e = 120 the largest code is 240's, since 256 * 2^120 is past
+ * float32: bf16 values beyond 3.3e38 are held as 3.19e38).  A block is coded when it is full; until then its tokens stay in bf16
  * in the row's tail buffer, so the cache's content depends on the tokens
  * alone, not on how they were split into calls.  Streaming heads hold bf16
  * rows: their ring overwrites slot by slot, which a block's scale could not

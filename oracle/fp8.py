@@ -6,6 +6,8 @@ KV cache only; this is the reading of an 8-bit one that ``duo.h`` states: per
 
     sc = 2^e, e the smallest integer >= -120 with max|x| <= 448 * 2^e  (finite x)
     code = e4m3 nearest to x / sc, ties to even, saturating at +-448, NaN kept
+           (at sc = 2^120 at +-240: a code of 256 would stand for 2^128, past
+           float32's range)
     x_hat = sc * code                                (exact in fp64)
 
 and tokens past the last full block are held as they are.  e4m3 has no
@@ -62,5 +64,7 @@ def held(x):
     y = x[:full].reshape(-1, BLOCK, heads, d).transpose(0, 2, 1, 3)  # [blocks, heads, BLOCK, d]
     sc = block_scale(y)
     codes = nearest_e4m3(y / sc[..., None, None])
+    top = (sc == 2.0 ** 120)[..., None, None]
+    codes = np.where(top, np.clip(codes, -240.0, 240.0), codes)
     out[:full] = (codes * sc[..., None, None]).transpose(0, 2, 1, 3).reshape(full, heads, d)
     return out, codes.transpose(0, 2, 1, 3).reshape(full, heads, d), sc

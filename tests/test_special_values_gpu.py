@@ -5,12 +5,16 @@ What a definition makes NaN is NaN, and what it does not touch keeps the bits
 of the same call without the special value.
 """
 
+import numpy as np
 import pytest
 import torch
 
 from head_split_kv_decode_b200 import binding as B
 from head_split_kv_decode_b200 import synth
 from head_split_kv_decode_b200.cache import DuoCache, merge_partials
+from oracle import fp8 as OF
+
+from _util import f64
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +111,58 @@ def test_decode_partials_keep_nan(cuda_lib, kv, splits):
     c.set_decode_splits(splits)
     for got in (out, c.decode(0, q).float()):
         assert got[0, (2, 6)].isnan().all() and torch.isfinite(got[0, live]).all()
+
+
+# ------------------------------------------------------------------ the largest values
+
+
+def _top_block():
+    """A block of 32 tokens around bf16's largest value, both signs, with the
+    values on either side of the cut and of code 240's neighbours, an infinity
+    and a NaN."""
+    big = 2.0 ** 120
+    vals = [torch.finfo(BF).max, 248 * big, 249 * big, 247 * big, 244 * big, 240 * big, 232 * big, 231 * big, 9 * big,
+            1.5 * 2.0 ** 111, 1e30, 0.0, INF, NAN]
+    x = torch.zeros(32, 1, D, dtype=torch.float64)
+    for i, y in enumerate(vals):
+        x[i, 0, i] = y
+        x[31 - i, 0, 64 + i] = -y
+    return x.to(BF).cuda()
+
+
+def test_largest_values_are_held_finite(cuda_lib):
+    """Every finite bf16 value is held as a finite one, up to the largest:
+    codes and scales bit for bit."""
+    x = _top_block()
+    assert torch.isfinite(x).sum() == x.numel() - 4
+    cache = DuoCache(1, 1, 1, 1, D, "fp8", 128, torch.ones(1, 1), 4, 60)
+    cache.append(0, x[None], x.flip(0)[None].contiguous())
+    torch.cuda.synchronize()
+    for name, y in (("k", x), ("v", x.flip(0))):
+        held, codes, sc = OF.held(f64(y))
+        assert np.isfinite(held[np.isfinite(f64(y))]).all() and np.nanmax(np.abs(held)) < 2.0 ** 128
+        got = cache.gather_rows(0, "ret_" + name, 0, 32)[0].cpu().numpy()
+        ref, nan = OF.encode_e4m3(codes)[:, 0], np.isnan(codes[:, 0])
+        assert np.array_equal(got[~nan], ref[~nan]) and ((got[nan] & 0x7F) == 0x7F).all()
+        gs = cache.gather_rows(0, "ret_%s_sz" % name, 0, 1).contiguous().view(torch.float32)
+        assert gs.item() == sc[0, 0] == 2.0 ** 120
+
+
+def test_largest_values_through_the_prefill(cuda_lib):
+    """A key or value of bf16's largest magnitude in the history: scores and
+    outputs stay finite where the held value makes them so."""
+    n, C = 64, 3
+    k, v, q = _seq(1, n + C, 1), _seq(2, n + C, 1), torch.zeros(C, 2, D, dtype=BF, device="cuda")
+    v[5, 0, 7] = torch.finfo(BF).max
+    k[9, 0, 3] = -torch.finfo(BF).max
+    cache = DuoCache(1, 1, 2, 1, D, "fp8", n + C, torch.ones(1, 1), 4, 60)
+    cache.append(0, k[None, :n], v[None, :n])
+    out = cache.prefill(0, q[None], k[None, n:].contiguous(), v[None, n:].contiguous())[0]
+    torch.cuda.synchronize()
+    # zero queries: every key has the same weight
+    held = np.concatenate([OF.held(f64(v[:n]))[0], f64(v[n:])])[:, 0]
+    for i in range(C):
+        ref = held[:n + i + 1].mean(0)
+        # equal probabilities are exact; the mean is rounded once, its fp32 sum is off by 2^-24 a term
+        tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * np.abs(held[:n + i + 1]).mean(0)
+        assert (np.abs(f64(out[i]) - ref[None]) <= tol[None]).all()
