@@ -22,6 +22,8 @@
 // a step 2^-11 of each) for the V product, relative to m - 7: with the lazy
 // rescale (m follows the running maximum when it grows by more than 2^8)
 // p <= 2^15 stays in range, and f16's smallest step is 2^-31 of the largest.
+// O takes U relative to m itself, so that values keep fp32's range (up to
+// 2^119 over the number of keys of a split, as in the bf16 decode).
 // bf16 rows (tail, streaming) use the same layout with bf16 operands, 16 keys
 // at a time; there p is rounded to bf16 (half a step 2^-8), V's own precision.
 //
@@ -45,7 +47,8 @@ namespace d8 {
 constexpr int D = 128;
 constexpr int NWARPS = 16;
 constexpr int T = kScaleBlock;      // keys per warp tile
-constexpr float kHeadroom = 7.f;    // p is taken relative to m - kHeadroom
+constexpr float kHeadroom = 7.f;    // p is taken relative to m - kHeadroom,
+constexpr float kUnscale = 1.f / 128.f;  // 2^-kHeadroom: O and l leave relative to m
 
 __device__ __forceinline__ uint4 ldg128(const void *p) {
   uint4 v;
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         p[e] = sc[h][e] == -INFINITY ? 0.f : fast_exp2(sc[h][e] - (mq[e] - kHeadroom));
         lq[e] += p[e];
       }
-      pb[h] = movm_trans(pack_bf16(p[0], p[1]));
+      pb[h] = movm_trans(pack_bf16(p[0] * kUnscale, p[1] * kUnscale));
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
@@ -428,6 +431,7 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         pb[kg][h] = movm_trans(pack_f16(p0, p1));
       }
     // ------------------------------------------- O^T += scale * (V^T P^T)
+    const float vu = vs * kUnscale;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
 #pragma unroll
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         }
         float(&od)[4] = o[2 * w + hh];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) od[i] = fmaf(vs, u[i], od[i]);
+        for (int i = 0; i < 4; ++i) od[i] = fmaf(vu, u[i], od[i]);
       }
   };
 
@@ -523,8 +527,8 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (2 * t + e < G) {
-        red_m[warp * G + 2 * t + e] = mq[e] - kHeadroom;  // the reference of l and O
-        red_l[warp * G + 2 * t + e] = lq[e];
+        red_m[warp * G + 2 * t + e] = mq[e];
+        red_l[warp * G + 2 * t + e] = lq[e] * kUnscale;
       }
   }
 #pragma unroll

@@ -166,3 +166,24 @@ def test_largest_values_through_the_prefill(cuda_lib):
         # equal probabilities are exact; the mean is rounded once, its fp32 sum is off by 2^-24 a term
         tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -17 * np.abs(held[:n + i + 1]).mean(0)
         assert (np.abs(f64(out[i]) - ref[None]) <= tol[None]).all()
+
+
+@pytest.mark.parametrize("splits", [0, 3])
+def test_large_values_through_the_decode(cuda_lib, splits):
+    """Values near the top of fp32's range: the decode's sums hold them as the
+    bf16 decode's do (300 keys of up to 2^118: under 2^127)."""
+    n = 300
+    k = _seq(1, n, 2)
+    v = ((1.0 + torch.rand(n, 2, D, generator=torch.Generator().manual_seed(2))) * 2.0 ** 117).to(BF).cuda()
+    q = torch.zeros(1, 4, D, dtype=BF, device="cuda")
+    cache = DuoCache(1, 1, 4, 2, D, "fp8", n, torch.tensor([[1, 0]]), 4, 290)
+    cache.set_decode_output(torch.float32)
+    cache.set_decode_splits(splits)
+    cache.append(0, k[None], v[None])
+    out = f64(cache.decode(0, q)[0])
+    # zero queries: every key has the same weight, a power of two, so that only the fp32 sums round
+    held = OF.held(f64(v))[0][:, 0], f64(v)[:, 1]
+    kept = np.arange(n)[(np.arange(n) < 4) | (np.arange(n) >= n - 290)]
+    for h in range(4):
+        ref = held[0].mean(0) if h < 2 else held[1][kept].mean(0)
+        assert (np.abs(out[h] - ref) <= 2.0 ** -15 * ref).all()
