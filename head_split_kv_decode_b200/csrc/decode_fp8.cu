@@ -18,21 +18,29 @@
 // and its V operand 16 consecutive channels of its keys.  Queries enter as
 // f16 too, scaled by a power of two per query so that the largest |q| lies in
 // [2^14, 2^15): what f16's range cuts off is below 2^-38 of it.
-// Probabilities are formed in fp32, summed in fp32, and rounded to f16 (half
-// a step 2^-11 of each) for the V product, relative to m - 7: with the lazy
+// Probabilities are formed and summed in fp32 and meet V as two f16 numbers,
+// the rounded value and what it lost (22 bits together; one f16 would be off by
+// 2^-11 of each and the outputs by up to 1e-3), relative to m - 7: with the lazy
 // rescale (m follows the running maximum when it grows by more than 2^8)
 // p <= 2^15 stays in range, and f16's smallest step is 2^-31 of the largest.
+// Of the product's eight columns G <= 4 queries leave the upper four idle:
+// they repeat the queries and carry the remainders, at no further product; for
+// more queries a second product takes them.  (One f16 against two, us: 128K
+// GQA 26.8 and 27.1, 1M 83.2 and 83.4, 300 tokens 6.4 and 6.7, 64K with eight
+// queries a head 20.0 to 21.4 and 20.7 to 21.0.)
 // O takes U relative to m itself, so that values keep fp32's range (up to
 // 2^119 over the number of keys of a split, as in the bf16 decode).
 // bf16 rows (tail, streaming) use the same layout with bf16 operands, 16 keys
-// at a time; there p is rounded to bf16 (half a step 2^-8), V's own precision.
+// at a time; there p is two bf16 numbers (16 bits).
 //
 // Bound: HBM, 256 bytes and 8/32 of a scale pair per key.  Measured on one
-// layer of 32/8 heads: 1M tokens, 2 retrieval heads: 83 us, 0.99 of the copy
-// rate; 128K, 4 retrieval heads: 26.5 us, 0.78 (18.4 us of main loop at 7.4
+// layer of 32/8 heads: 1M tokens, 2 retrieval heads: 83.4 us, 0.98 of the copy
+// rate; 128K, 4 retrieval heads: 27.1 us, 0.76 (about 18.4 us of main loop at 7.4
 // TB/s, the rest is the way to the first tile, the reduction and the merge).
+// 128 registers a thread: each variant spills a few (36 to 60 bytes; G = 1, which
+// computes one of a thread's two columns, 48).
 // 32 keys a tile and single-buffered registers: 16 keys loaded a tile ahead
-// spill and double the per-tile work (33.0 us at 128K), and the 16 warps'
+// spill more and double the per-tile work (33.0 us at 128K), and the 16 warps'
 // loads, 128 KB an SM, leave no room for a prefetch to help (1M 86 us with).
 //
 // Pages: "DuoAttention: Efficient Long-Context LLM Inference with Retrieval and
@@ -124,6 +132,11 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   __shared__ __align__(16) uint32_t s_qb[kMaxStrPack * 4 * 32 * 4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;  // mma fragment coordinates
+  // G <= 4: columns 4..7 repeat the queries 0..3 and carry what their
+  // probabilities lose in rounding; else a second product does
+  constexpr bool kFold = G <= 4;
+  const bool rest = kFold && t >= 2;  // this thread's two columns are remainders
+  constexpr int E = G == 1 ? 1 : 2;   // columns of a thread that can hold a query
 
   // ---- work item: retrieval CTAs first (launch row, head, split), then per
   // launch row the streaming CTAs of str_pack heads each
@@ -230,9 +243,10 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   float c1[2];  // score factor (log2 units) of queries 2t, 2t+1 on raw f16 sums
   const float sl2 = P.scale_log2;
   {
+    const int gq = kFold ? g & 3 : g;
     const __nv_bfloat16 *qrow =
-        reinterpret_cast<const __nv_bfloat16 *>(P.q) + ((int64_t)r * P.Hq + (int64_t)kvh * G + g) * D;
-    const bool live = g < G;
+        reinterpret_cast<const __nv_bfloat16 *>(P.q) + ((int64_t)r * P.Hq + (int64_t)kvh * G + gq) * D;
+    const bool live = gq < G;
     if (wsub == 0 || retrieval) {
       // bf16: 16-byte chunk 32c + 8t (c = 0..3), words = k-steps 2c (2), 2c+1 (2)
       if (wsub == 0) {
@@ -298,12 +312,13 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   // Raise the running maxima to cover a tile whose own largest scores (this
   // thread's keys) are mx; needed only when some lane passes m + 8.
   auto raise = [&](float (&mx)[2]) {
-    if (!__any_sync(0xffffffffu, mx[0] > mq[0] + 8.f || mx[1] > mq[1] + 8.f)) return;
+    if (!__any_sync(0xffffffffu, mx[0] > mq[0] + 8.f || (E > 1 && mx[1] > mq[1] + 8.f))) return;
     float alpha[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < E; ++e) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
+      for (int off = kFold ? 2 : 4; off < 32; off <<= 1)  // (2: a query and its remainder keep one m)
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
       alpha[e] = 1.f;
       if (mx[e] > mq[e] + 8.f) {
         alpha[e] = mq[e] == -INFINITY ? 0.f : fast_exp2(mq[e] - mx[e]);
@@ -315,8 +330,10 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
     for (int i = 0; i < 8; ++i) {
       o[i][0] *= alpha[0];
       o[i][2] *= alpha[0];
-      o[i][1] *= alpha[1];
-      o[i][3] *= alpha[1];
+      if constexpr (E > 1) {
+        o[i][1] *= alpha[1];
+        o[i][3] *= alpha[1];
+      }
     }
   };
 
@@ -354,24 +371,30 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
     mx[0] = fmaxf(sc[0][0], sc[1][0]);
     mx[1] = fmaxf(sc[0][1], sc[1][1]);
     raise(mx);
-    uint32_t pb[2];
+    uint32_t pb[2], pr[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float p[2];
+      float p[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[e] = sc[h][e] == -INFINITY ? 0.f : fast_exp2(sc[h][e] - (mq[e] - kHeadroom));
-        lq[e] += p[e];
+      for (int e = 0; e < E; ++e) {
+        p[e] = sc[h][e] == -INFINITY ? 0.f : fast_exp2(sc[h][e] - mq[e]);
+        lq[e] = fmaf(p[e], 1.f / kUnscale, lq[e]);
       }
-      pb[h] = movm_trans(pack_bf16(p[0] * kUnscale, p[1] * kUnscale));
+      const uint32_t hi = pack_bf16(p[0], p[1]);
+      const float2 f = bf16x2_to_f2(hi);
+      const uint32_t lo = pack_bf16(p[0] - f.x, p[1] - f.y);
+      pb[h] = movm_trans(rest ? lo : hi);
+      if (!kFold) pr[h] = movm_trans(lo);
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = (&vr[i][mt >> 2].x)[mt & 3];
-      mma_bf16(o[mt], __byte_perm(w[0], w[1], 0x5410u), __byte_perm(w[0], w[1], 0x7632u),
-               __byte_perm(w[2], w[3], 0x5410u), __byte_perm(w[2], w[3], 0x7632u), pb[0], pb[1]);
+      const uint32_t a[4] = {__byte_perm(w[0], w[1], 0x5410u), __byte_perm(w[0], w[1], 0x7632u),
+                             __byte_perm(w[2], w[3], 0x5410u), __byte_perm(w[2], w[3], 0x7632u)};
+      mma_bf16(o[mt], a[0], a[1], a[2], a[3], pb[0], pb[1]);
+      if (!kFold) mma_bf16(o[mt], a[0], a[1], a[2], a[3], pr[0], pr[1]);
     }
   };
 
@@ -414,21 +437,26 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
 #pragma unroll
     for (int kg = 0; kg < 2; ++kg)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; i += 3 - E) {
         acc[kg][i] *= f[i & 1];
         mx[i & 1] = fmaxf(mx[i & 1], acc[kg][i]);
       }
     raise(mx);
-    uint32_t pb[2][2];
+    uint32_t pb[2][2], pr[2][2];
     const float ref[2] = {mq[0] - kHeadroom, mq[1] - kHeadroom};
 #pragma unroll
     for (int kg = 0; kg < 2; ++kg)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float p0 = fast_exp2(acc[kg][2 * h] - ref[0]), p1 = fast_exp2(acc[kg][2 * h + 1] - ref[1]);
+        const float p0 = fast_exp2(acc[kg][2 * h] - ref[0]);
+        const float p1 = E > 1 ? fast_exp2(acc[kg][2 * h + 1] - ref[1]) : 0.f;
         lq[0] += p0;
-        lq[1] += p1;
-        pb[kg][h] = movm_trans(pack_f16(p0, p1));
+        if constexpr (E > 1) lq[1] += p1;
+        const uint32_t hi = pack_f16(p0, p1);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        const uint32_t lo = pack_f16(p0 - f.x, p1 - f.y);
+        pb[kg][h] = movm_trans(rest ? lo : hi);
+        if (!kFold) pr[kg][h] = movm_trans(lo);
       }
     // ------------------------------------------- O^T += scale * (V^T P^T)
     const float vu = vs * kUnscale;
@@ -443,11 +471,13 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
           // (channel 2mt: keys 2t, 2t+1) low, (channel 2mt + 1) high
           const uint32_t ab = __byte_perm((&vr[kg][0].x)[w], (&vr[kg][1].x)[w], sel);
           const uint32_t cd = __byte_perm((&vr[kg][2].x)[w], (&vr[kg][3].x)[w], sel);
-          mma_f16(u, f16x2_lo(ab), f16x2_hi(ab), f16x2_lo(cd), f16x2_hi(cd), pb[kg][0], pb[kg][1]);
+          const uint32_t a[4] = {f16x2_lo(ab), f16x2_hi(ab), f16x2_lo(cd), f16x2_hi(cd)};
+          mma_f16(u, a[0], a[1], a[2], a[3], pb[kg][0], pb[kg][1]);
+          if (!kFold) mma_f16(u, a[0], a[1], a[2], a[3], pr[kg][0], pr[kg][1]);
         }
         float(&od)[4] = o[2 * w + hh];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) od[i] = fmaf(vu, u[i], od[i]);
+        for (int i = 0; i < 4; i += 3 - E) od[i] = fmaf(vu, u[i], od[i]);
       }
   };
 
@@ -520,12 +550,12 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   float *red_l = red_m + NWARPS * G;
   float *red_o = red_l + NWARPS * G;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < E; ++e)
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) lq[e] += __shfl_xor_sync(0xffffffffu, lq[e], off);
   if (g == 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < E; ++e)
       if (2 * t + e < G) {
         red_m[warp * G + 2 * t + e] = mq[e];
         red_l[warp * G + 2 * t + e] = lq[e] * kUnscale;
@@ -535,8 +565,14 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   for (int mt = 0; mt < 8; ++mt) {
     const int ch = 16 * g + 2 * mt;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (2 * t + e < G) {
+    for (int e = 0; e < E; ++e)
+      if constexpr (kFold) {
+        // query and remainder meet: threads t < 2 finish the tile's even
+        // channels, their partners t + 2 the odd ones
+        const float got = __shfl_xor_sync(0xffffffffu, rest ? o[mt][e] : o[mt][2 + e], 2);
+        const int q = (2 * t + e) & 3;
+        if (q < G) red_o[(warp * G + q) * D + ch + rest] = (rest ? o[mt][2 + e] : o[mt][e]) + got;
+      } else if (2 * t + e < G) {
         red_o[(warp * G + 2 * t + e) * D + ch] = o[mt][e];
         red_o[(warp * G + 2 * t + e) * D + ch + 1] = o[mt][2 + e];
       }

@@ -1,5 +1,5 @@
-"""NaN, infinities and values at the ends of the types' ranges through the
-rotary and 8-bit cache operators.
+"""NaN, infinities, values at the ends of the types' ranges, and the bits of a
+probability, through the rotary and 8-bit cache operators.
 
 What a definition makes NaN is NaN, and what it does not touch keeps the bits
 of the same call without the special value.
@@ -12,6 +12,7 @@ import torch
 from head_split_kv_decode_b200 import binding as B
 from head_split_kv_decode_b200 import synth
 from head_split_kv_decode_b200.cache import DuoCache, merge_partials
+from oracle import attention as OA
 from oracle import fp8 as OF
 
 from _util import f64
@@ -187,3 +188,29 @@ def test_large_values_through_the_decode(cuda_lib, splits):
     for h in range(4):
         ref = held[0].mean(0) if h < 2 else held[1][kept].mean(0)
         assert (np.abs(out[h] - ref) <= 2.0 ** -15 * ref).all()
+
+
+@pytest.mark.parametrize("group", range(1, 9))
+def test_decode_keeps_the_probabilities_bits(cuda_lib, group):
+    """Every channel holds one key's value, so that each output is one
+    probability times it.  Queries have one channel: a score is one exact
+    product, |score| log2(e) <= 6, times the scale (4 roundings: 2^-20).  A
+    probability is off by that and the exponential's 2^-21, kept to 2^-16 (two
+    bf16; two f16 keep more), over a sum of at most 117 (2^-17): 2^-15 in all."""
+    n, S, R = 117, 4, 100
+    k = _seq(1, n, 2)
+    k[:, :, 0] = (8.0 * torch.rand(n, 2, generator=torch.Generator().manual_seed(4)) - 4.0).to(BF).cuda()
+    v = torch.zeros(n, 2, D, dtype=BF, device="cuda")
+    at = torch.arange(n, device="cuda")
+    v[at, :, at] = (1.0 + torch.rand(n, 2, generator=torch.Generator().manual_seed(5))).to(BF).cuda()
+    q = torch.zeros(1, 2 * group, D, dtype=BF, device="cuda")
+    q[0, :, 0] = torch.linspace(-1.0, 1.0, 2 * group).to(BF).cuda()
+    mask = torch.tensor([1, 0])
+    cache = DuoCache(1, 1, 2 * group, 2, D, "fp8", n, mask[None], S, R)
+    cache.set_decode_output(torch.float32)
+    cache.append(0, k[None], v[None])
+    kh, vh = f64(k), f64(v)
+    kh[:, 0], vh[:, 0] = OF.held(kh)[0][:, 0], OF.held(vh)[0][:, 0]
+    ref = OA.decode_reference(f64(q), kh[None], vh[None], mask.numpy(), S, R, 1.0)
+    out = f64(cache.decode(0, q, scale=1.0))
+    assert (np.abs(out - ref) <= 2.0 ** -15 * ref).all()
