@@ -148,7 +148,8 @@ __device__ __forceinline__ Quads quads_of(const RopeParams &r, int sl) {
 
 // inv_freq / (2 pi) as a 64-bit fraction of a turn, modulo whole turns: the
 // 24-bit significand times the leading 64 bits of 1 / (2 pi) (scaled by 2^66),
-// shifted by the exponent.  Off by at most 2 units of 2^-64.
+// shifted by the exponent.  Off by less than |inv_freq| / 4 + 1 units of 2^-64
+// (the constant's truncation and the shift's); of finite frequencies only.
 __device__ __forceinline__ uint64_t turn_rate(float inv_freq) {
   constexpr uint64_t kInvTwoPi = 0xA2F9836E4E441529ull;
   const uint32_t u = __float_as_uint(inv_freq);
@@ -212,14 +213,15 @@ __device__ __forceinline__ void fill_angles(const RopeParams &r, float *s_cos, f
     need[k] = first + k * kPer < NT && pos(first + k * kPer, p[k]);
   }
   const bool turns = pair < (r.rot_dim >> 1);
-  const uint64_t rate = turns ? turn_rate(r.inv_freq[pair]) : 0;
+  const float freq = turns ? r.inv_freq[pair] : 0.f;
+  const uint64_t rate = turn_rate(freq);
+  const float ms = turns ? r.mscale + (freq - freq) : 1.f;  // NaN where the frequency is not finite
 #pragma unroll
   for (int k = 0; k < kIt; ++k) {
     if (!need[k]) continue;
-    float2 cs = cos_sin(p[k], rate);
-    if (turns) cs.x *= r.mscale, cs.y *= r.mscale;
-    s_cos[threadIdx.x + k * THREADS] = cs.x;  // pair's column of token first + k * kPer
-    s_sin[threadIdx.x + k * THREADS] = cs.y;
+    const float2 cs = cos_sin(p[k], rate);
+    s_cos[threadIdx.x + k * THREADS] = cs.x * ms;  // pair's column of token first + k * kPer
+    s_sin[threadIdx.x + k * THREADS] = cs.y * ms;
   }
 }
 

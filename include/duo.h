@@ -237,8 +237,11 @@ typedef struct duo_heads {
  *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s),
  *   c + i s = mscale * exp(i * position * inv_freq[j])
  * for pair j of the first rot_dim channels: (a, b) = (j, j + rot_dim/2), or
- * (2j, 2j + 1) when interleaved.  fp32 throughout (the angle in 64 bits, so
- * that far positions keep their phase), rounded once to the tensors' type. */
+ * (2j, 2j + 1) when interleaved.  fp32 throughout, rounded once to the
+ * tensors' type.  The angle is a 64-bit fixed-point fraction of a turn, so that
+ * far positions keep their phase: off by less than 2^-26 radian while
+ * |position| * max(|inv_freq|, 8) < 2^36.  A frequency that is not finite makes
+ * its pair's channels NaN. */
 typedef struct duo_rope_desc {
   int32_t rot_dim;       /* 0 (no rotation) .. head_dim, a multiple of 16 */
   int32_t interleaved;   /* 0 or 1 */

@@ -12,10 +12,12 @@ import torch
 from head_split_kv_decode_b200 import binding as B
 from head_split_kv_decode_b200 import synth
 from head_split_kv_decode_b200.cache import DuoCache, merge_partials
+from head_split_kv_decode_b200.rotary import Rotary, qk_norm_rope
 from oracle import attention as OA
 from oracle import fp8 as OF
 
 from _util import f64
+from test_rotary_gpu import assert_rotated
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +216,54 @@ def test_decode_keeps_the_probabilities_bits(cuda_lib, group):
     ref = OA.decode_reference(f64(q), kh[None], vh[None], mask.numpy(), S, R, 1.0)
     out = f64(cache.decode(0, q, scale=1.0))
     assert (np.abs(out - ref) <= 2.0 ** -15 * ref).all()
+
+
+# ------------------------------------------------------------------ frequencies
+
+
+@pytest.mark.parametrize("start", [0, -1000003, 12345678, (1 << 33) - 100])
+def test_frequencies_of_every_size(cuda_lib, start):
+    """Negative, zero and subnormal frequencies, and many radians a position,
+    while |position| * max(|frequency|, 8) < 2^36."""
+    n, rot = 33, 64
+    f = [4.0, 4.0000005, 7.75, -3.0, -0.3, 0.0, 1e-40, -1e-45, 1.17549435e-38, 1e-20, 5e-7, 1.9999999, 2.0, 3.1415927,
+         6.2831855, 1.0 / 3.0]
+    f += [100.25, -1000.1, 4096.5, 0.1, 0.2, 0.7, 1e-3, 2.5] if abs(start) < 1 << 24 else [7.9, 0.11] * 4
+    f += [0.01 * i for i in range(8)]
+    freq = torch.tensor(f, dtype=torch.float32, device="cuda")
+    pos = start + torch.arange(n, dtype=torch.int64, device="cuda")
+    assert (pos.abs().max().double() * freq.abs().clamp(min=8).max().double()).item() < 2.0 ** 36
+    x = _seq(7, n, 3)
+    for il in (False, True):
+        o, _ = qk_norm_rope(Rotary(freq, D, interleaved=il), x, None, pos)
+        torch.cuda.synchronize()
+        assert_rotated(o, x, pos.cpu().numpy(), rot, None, 0.0, freq, il, 1.0)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("il", [False, True])
+def test_a_frequency_that_is_not_finite(cuda_lib, il, bad):
+    """Its pair is NaN at every position, the others keep their bits; alone and
+    on the way into an 8-bit cache, row by row and as whole blocks."""
+    n, rot = 40, 64
+    freq = (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().cuda()
+    broken = freq.clone()
+    broken[5] = bad
+    pair = [10, 11] if il else [5, 5 + rot // 2]
+    rest = [c for c in range(D) if c not in pair]
+    q, k = _seq(8, n, 2), _seq(9, n, 1)
+    pos = torch.arange(n, device="cuda")
+    ref = qk_norm_rope(Rotary(freq, D, interleaved=il), q, k, pos)
+    out = qk_norm_rope(Rotary(broken, D, interleaved=il), q, k, pos)
+    for a, b in zip(out, ref):
+        assert a[:, :, pair].isnan().all() and torch.equal(a[:, :, rest], b[:, :, rest])
+    cache = DuoCache(1, 1, 2, 1, D, "fp8", 128, torch.ones(1, 1), 4, 60)
+    r = Rotary(broken, D, interleaved=il)
+    for a, b in ((0, 3), (3, n)):
+        got = cache.append_rope(0, r, k[None, a:b], k[None, a:b], q=q[None, a:b])[0]
+        assert got[:, :, pair].isnan().all() and torch.equal(got[:, :, rest], ref[0][a:b][:, :, rest])
+    torch.cuda.synchronize()
+    codes = cache.gather_rows(0, "ret_k", 0, 32)[0]
+    assert ((codes[:, pair] & 0x7F) == 0x7F).all() and ((codes[:, rest] & 0x7F) != 0x7F).all()
+    tail = cache.region(0, "tail_k").view(BF)[0, 0, :n - 32]
+    assert tail[:, pair].isnan().all() and torch.equal(tail[:, rest], ref[1][32:, 0][:, rest])
