@@ -367,13 +367,14 @@ class DuoCache:
         return self.storage[off:off + nbytes].view(outer, heads, rows, width)
 
     def gather_rows(self, layer, name, row, n):
-        """The first n retrieval rows of one batch row, in position order, as
-        [heads, n, width] (packed: a slice; paged: through the block table).
+        """The first n rows of one buffer of one batch row as [heads, n, width]:
+        retrieval rows in position order (packed: a slice; paged: through the
+        block table), slots of a streaming or tail buffer as they lie.
         Rows of an 8-bit cache's scales stand for FP8_BLOCK tokens each."""
         reg = self.region(layer, name)
         if reg is None:
             return None
-        if not self.paged:
+        if not self.paged or not name.startswith("ret"):
             return reg[row, :, :n]
         if n == 0:
             return reg[0, :, :0]
