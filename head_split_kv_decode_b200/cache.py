@@ -22,12 +22,6 @@ def _aligned_buffer(nbytes, device, zero):
     return buf, off
 
 
-def _stream_handle(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 class DuoCache:
     """A head-split KV cache for ``layers`` layers bound to torch-allocated memory.
 
@@ -63,7 +57,8 @@ class DuoCache:
         self._storage, off = _aligned_buffer(self.cache_bytes, self.device, zero=False)
         self.base_ptr = self._storage.data_ptr() + off
         self.storage = self._storage[off:off + self.cache_bytes]
-        B.duo_cache_bind(self.handle, self.base_ptr, self.cache_bytes)
+        with torch.cuda.device(self.device):
+            B.duo_cache_bind(self.handle, self.base_ptr, self.cache_bytes)
         self._ws, woff = _aligned_buffer(self.ws_bytes, self.device, zero=True)
         self.ws_ptr = self._ws.data_ptr() + woff
         self.prefill_ws_bytes = B.duo_prefill_workspace_bytes(self.handle)
@@ -92,15 +87,24 @@ class DuoCache:
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
 
+    def _out(self, out, like, shape, dtype=None, name="out"):
+        """out, checked, or a new tensor of the stream that is current."""
+        if out is None:
+            return like.new_empty(shape, dtype=dtype or self.io_dtype)
+        self._check(out, shape, name, dtype)
+        return out
+
     # ------------------------------------------------------------ calls
+    # Each launch runs with the cache's device current, where its memory lies,
+    # and what it allocates belongs to its stream (rotary.run_on).
     def append(self, layer, k, v, stream=None):
         """k, v: [batch, n_tokens, n_kv_heads, head_dim]."""
         n = k.shape[1]
         shape = (self.batch, n, self.n_kv_heads, self.head_dim)
         self._check(k, shape, "k")
         self._check(v, shape, "v")
-        B.duo_append_kv(self.handle, layer, k.data_ptr(), v.data_ptr(), n,
-                        _stream_handle(stream, self.device))
+        run_on(self.device, stream, lambda handle: B.duo_append_kv(
+            self.handle, layer, k.data_ptr(), v.data_ptr(), n, handle))
 
     def append_rope(self, layer, rotary, k, v, q=None, positions=None, q_out=None, stream=None):
         """:meth:`append` with k normed and rotated on the way by ``rotary``
@@ -161,12 +165,14 @@ class DuoCache:
         """q: [batch, n_q_heads, head_dim] at position seq_len-1.  Returns out."""
         shape = (self.batch, self.n_q_heads, self.head_dim)
         self._check(q, shape, "q")
-        if out is None:
-            out = q.new_empty(shape, dtype=self.out_dtype)
-        self._check(out, shape, "out", self.out_dtype)
-        B.duo_decode_attn(self.handle, layer, q.data_ptr(), out.data_ptr(), float(scale),
-                          self.ws_ptr, self.ws_bytes, _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, shape, self.out_dtype)
+            B.duo_decode_attn(self.handle, layer, q.data_ptr(), o.data_ptr(), float(scale),
+                              self.ws_ptr, self.ws_bytes, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     def step(self, layer, q, k_new, v_new, out=None, scale=0.0, stream=None):
         """Append one token (k_new, v_new: [batch, n_kv_heads, head_dim]) and
@@ -176,13 +182,14 @@ class DuoCache:
         self._check(q, shape, "q")
         self._check(k_new, kv_shape, "k_new")
         self._check(v_new, kv_shape, "v_new")
-        if out is None:
-            out = q.new_empty(shape, dtype=self.out_dtype)
-        self._check(out, shape, "out", self.out_dtype)
-        B.duo_decode_step(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                          out.data_ptr(), float(scale), self.ws_ptr, self.ws_bytes,
-                          _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, shape, self.out_dtype)
+            B.duo_decode_step(self.handle, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                              o.data_ptr(), float(scale), self.ws_ptr, self.ws_bytes, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     def prefill(self, layer, q, k, v, out=None, scale=0.0, stream=None):
         """q: [batch, C, n_q_heads, d]; k, v: [batch, C, n_kv_heads, d].  Attends only."""
@@ -190,14 +197,15 @@ class DuoCache:
         self._check(q, (self.batch, C, self.n_q_heads, self.head_dim), "q")
         self._check(k, (self.batch, C, self.n_kv_heads, self.head_dim), "k")
         self._check(v, (self.batch, C, self.n_kv_heads, self.head_dim), "v")
-        if out is None:
-            out = torch.empty_like(q)
-        self._check(out, tuple(q.shape), "out")
-        ws, wsb = self._prefill_ws()
-        B.duo_prefill_attn(self.handle, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(), C,
-                           out.data_ptr(), float(scale), ws, wsb,
-                           _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, q.shape)
+            ws, wsb = self._prefill_ws()
+            B.duo_prefill_attn(self.handle, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(), C,
+                               o.data_ptr(), float(scale), ws, wsb, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     # ------------------------------------------------------------ row calls
     def _rows(self, rows):
@@ -213,20 +221,22 @@ class DuoCache:
         shape = (len(rows), n, self.n_kv_heads, self.head_dim)
         self._check(k, shape, "k")
         self._check(v, shape, "v")
-        B.duo_append_kv_rows(self.handle, layer, rows, k.data_ptr(), v.data_ptr(), n,
-                             _stream_handle(stream, self.device))
+        run_on(self.device, stream, lambda handle: B.duo_append_kv_rows(
+            self.handle, layer, rows, k.data_ptr(), v.data_ptr(), n, handle))
 
     def decode_rows(self, layer, rows, q, out=None, scale=0.0, stream=None):
         """q: [len(rows), n_q_heads, head_dim], each row's query at its last position."""
         rows = self._rows(rows)
         shape = (len(rows), self.n_q_heads, self.head_dim)
         self._check(q, shape, "q")
-        if out is None:
-            out = q.new_empty(shape, dtype=self.out_dtype)
-        self._check(out, shape, "out", self.out_dtype)
-        B.duo_decode_attn_rows(self.handle, layer, rows, q.data_ptr(), out.data_ptr(), float(scale),
-                               self.ws_ptr, self.ws_bytes, _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, shape, self.out_dtype)
+            B.duo_decode_attn_rows(self.handle, layer, rows, q.data_ptr(), o.data_ptr(), float(scale),
+                                   self.ws_ptr, self.ws_bytes, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     def step_rows(self, layer, rows, q, k_new, v_new, out=None, scale=0.0, stream=None):
         """Append one token to each listed row and attend (see :meth:`step`)."""
@@ -236,13 +246,15 @@ class DuoCache:
         self._check(q, shape, "q")
         self._check(k_new, kv_shape, "k_new")
         self._check(v_new, kv_shape, "v_new")
-        if out is None:
-            out = q.new_empty(shape, dtype=self.out_dtype)
-        self._check(out, shape, "out", self.out_dtype)
-        B.duo_decode_step_rows(self.handle, layer, rows, q.data_ptr(), k_new.data_ptr(),
-                               v_new.data_ptr(), out.data_ptr(), float(scale), self.ws_ptr,
-                               self.ws_bytes, _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, shape, self.out_dtype)
+            B.duo_decode_step_rows(self.handle, layer, rows, q.data_ptr(), k_new.data_ptr(),
+                                   v_new.data_ptr(), o.data_ptr(), float(scale), self.ws_ptr,
+                                   self.ws_bytes, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     def prefill_rows(self, layer, rows, q, k, v, out=None, scale=0.0, stream=None):
         """q: [len(rows), C, n_q_heads, d]; k, v: [len(rows), C, n_kv_heads, d]."""
@@ -251,14 +263,15 @@ class DuoCache:
         self._check(q, (len(rows), C, self.n_q_heads, self.head_dim), "q")
         self._check(k, (len(rows), C, self.n_kv_heads, self.head_dim), "k")
         self._check(v, (len(rows), C, self.n_kv_heads, self.head_dim), "v")
-        if out is None:
-            out = torch.empty_like(q)
-        self._check(out, tuple(q.shape), "out")
-        ws, wsb = self._prefill_ws()
-        B.duo_prefill_attn_rows(self.handle, layer, rows, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                C, out.data_ptr(), float(scale), ws, wsb,
-                                _stream_handle(stream, self.device))
-        return out
+
+        def call(handle):
+            o = self._out(out, q, q.shape)
+            ws, wsb = self._prefill_ws()
+            B.duo_prefill_attn_rows(self.handle, layer, rows, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                    C, o.data_ptr(), float(scale), ws, wsb, handle)
+            return o
+
+        return run_on(self.device, stream, call)
 
     # ------------------------------------------------------------ sequence shards
     def set_retrieval_shard(self, lo, hi):
@@ -271,16 +284,15 @@ class DuoCache:
         lse_part f32 [batch, Hq]) to merge with :func:`merge_partials`."""
         shape = (self.batch, self.n_q_heads, self.head_dim)
         self._check(q, shape, "q")
-        if o_part is None:
-            o_part = torch.empty(shape, dtype=torch.float32, device=q.device)
-        if lse_part is None:
-            lse_part = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-        self._check(o_part, shape, "o_part", torch.float32)
-        self._check(lse_part, shape[:2], "lse_part", torch.float32)
-        B.duo_decode_attn_partial(self.handle, layer, q.data_ptr(), o_part.data_ptr(),
-                                  lse_part.data_ptr(), owns_streaming, float(scale), self.ws_ptr,
-                                  self.ws_bytes, _stream_handle(stream, self.device))
-        return o_part, lse_part
+
+        def call(handle):
+            o = self._out(o_part, q, shape, torch.float32, "o_part")
+            lse = self._out(lse_part, q, shape[:2], torch.float32, "lse_part")
+            B.duo_decode_attn_partial(self.handle, layer, q.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                      owns_streaming, float(scale), self.ws_ptr, self.ws_bytes, handle)
+            return o, lse
+
+        return run_on(self.device, stream, call)
 
     def release_rows(self, rows=None):
         B.duo_release_rows(self.handle, None if rows is None else self._rows(rows))
@@ -410,7 +422,8 @@ def merge_partials(o_parts, lse_parts, out, stream=None):
     kind = {torch.bfloat16: "bf16", torch.float32: "f32"}.get(out.dtype)
     if kind is None:
         raise ValueError("out must be bfloat16 or float32")
-    s = stream if stream is not None else torch.cuda.current_stream(out.device)
-    B.duo_merge_partials(n, rows, d, o_parts.data_ptr(), lse_parts.data_ptr(), out.data_ptr(), kind,
-                         s.cuda_stream)
+    if o_parts.device != out.device or lse_parts.device != out.device:
+        raise ValueError("partials and output must be on one device")
+    run_on(out.device, stream, lambda handle: B.duo_merge_partials(
+        n, rows, d, o_parts.data_ptr(), lse_parts.data_ptr(), out.data_ptr(), kind, handle))
     return out

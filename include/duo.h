@@ -39,7 +39,8 @@
  *    the K/V/Q/O of a DUO_INT4 cache (K/V are quantised on append).  Decode
  *    outputs of bf16 and 4-bit caches can be float32 instead
  *    (duo_set_decode_output).
- *  - Every call with a stream is asynchronous on that stream.  Argument,
+ *  - Every call with a stream is asynchronous on that stream, which belongs to
+ *    the current device: the one that holds the call's tensors.  Argument,
  *    capacity and layout errors are detected on the host and returned before
  *    anything is enqueued; a failed launch returns DUO_ERR_CUDA.  Nothing
  *    throws across this boundary.  Calls on one cache must be ordered by the
