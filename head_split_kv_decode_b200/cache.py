@@ -57,10 +57,10 @@ class DuoCache:
         self._storage, off = _aligned_buffer(self.cache_bytes, self.device, zero=False)
         self.base_ptr = self._storage.data_ptr() + off
         self.storage = self._storage[off:off + self.cache_bytes]
-        with torch.cuda.device(self.device):
-            B.duo_cache_bind(self.handle, self.base_ptr, self.cache_bytes)
         self._ws, woff = _aligned_buffer(self.ws_bytes, self.device, zero=True)
         self.ws_ptr = self._ws.data_ptr() + woff
+        with torch.cuda.device(self.device):  # (waits for the device: the workspace is zero for any stream)
+            B.duo_cache_bind(self.handle, self.base_ptr, self.cache_bytes)
         self.prefill_ws_bytes = B.duo_prefill_workspace_bytes(self.handle)
         self._pf_ws, self.pf_ws_ptr = None, None
         self._regions = {}

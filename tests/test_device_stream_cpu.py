@@ -110,3 +110,24 @@ def test_given_outputs_are_used(world):
     o, lse = Fake(now, 2, 8, 128), Fake(now, 2, 8)
     got = c.decode_partial(0, Fake(now, 2, 8, 128), o_part=o, lse_part=lse)
     assert got[0] is o and got[1] is lse
+
+
+def test_workspace_is_zero_before_the_cache_is_bound(world, monkeypatch):
+    """Binding waits for the device, so a first decode on any stream finds the
+    workspace's zeros if they were asked for before it."""
+    now, calls, _ = world
+    order = []
+
+    def buffer(n, device, zero):
+        order.append("zeros" if zero else "memory")
+        t = Fake(now, n)
+        t.__class__ = type("Buffer", (Fake,), {"__getitem__": lambda self, i: self})
+        return t, 0
+    monkeypatch.setattr(C, "_aligned_buffer", buffer)
+    monkeypatch.setattr(B, "duo_cache_create", lambda *a: 1)
+    monkeypatch.setattr(B, "duo_cache_required_bytes", lambda h: (100, 100))
+    monkeypatch.setattr(B, "duo_cache_bind", lambda *a: order.append("bind on %d" % now["device"]))
+    monkeypatch.setattr(B, "duo_prefill_workspace_bytes", lambda h: 0)
+    monkeypatch.setattr(B, "duo_cache_destroy", lambda h: None)
+    C.DuoCache(1, 1, 2, 1, 128, "bf16", 64, [[1]], 4, 16, device=HERE)
+    assert sorted(order[:-1]) == ["memory", "zeros"] and order[-1] == "bind on 1"
