@@ -205,6 +205,16 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
       : "memory");
 }
 
+// Likewise from a 4-D map.
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- tile schedule
 //
 // The key tiles one query pair visits, in order: tiles of the cache prefix
@@ -286,7 +296,7 @@ struct Sched {
 
 struct Maps {
   CUtensorMap q;       // [B*C][Hq][D]
-  CUtensorMap kc, vc;  // [B*C][Hkv][D]     (chunk K/V)
+  CUtensorMap kc, vc;  // [B][C][Hkv][D]    (chunk K/V; a tile past a row's C tokens reads zeros)
   CUtensorMap kr, vr;  // [B*n_ret][cap][D] (retrieval pages)
   CUtensorMap ks, vs;  // [B*n_str][W][D]   (streaming slot buffers)
 };
@@ -420,9 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load3(dst + BOX, m, 64, y, z, fb);
         } else {
           const CUtensorMap *m = is_v ? &M.vc : &M.kc;
-          const int z = b * P.C + idx * BN;
-          tma_load3(dst, m, 0, kvh, z, fb);
-          tma_load3(dst + BOX, m, 64, kvh, z, fb);
+          tma_load4(dst, m, 0, kvh, idx * BN, b, fb);
+          tma_load4(dst + BOX, m, 64, kvh, idx * BN, b, fb);
         }
         return true;
       };
@@ -729,16 +738,17 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D bf16 map over [d2][d1][128] with a box of (64, b1, b2), 128-byte swizzle.
+// 3-D bf16 map over [d2][d1][128] with a box of (64, b1, b2), 128-byte swizzle;
+// with d3, 4-D over [d3][d2][d1][128], one index of d3 a box.
 static bool make_map(CUtensorMap *m, const void *ptr, uint64_t d1, uint64_t d2, uint64_t stride1,
-                     uint64_t stride2, uint32_t b1, uint32_t b2) {
+                     uint64_t stride2, uint32_t b1, uint32_t b2, uint64_t d3 = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc || !ptr) return false;
-  const cuuint64_t dims[3] = {HD, d1, d2};
-  const cuuint64_t strides[2] = {stride1, stride2};
-  const cuuint32_t box[3] = {64, b1, b2};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+  const cuuint64_t dims[4] = {HD, d1, d2, d3};
+  const cuuint64_t strides[3] = {stride1, stride2, stride2 * d2};
+  const cuuint32_t box[4] = {64, b1, b2, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d3 ? 4 : 3, const_cast<void *>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -795,8 +805,8 @@ static cudaError_t launch(const PrefillParams &p, const PrefillSplit &x, cudaStr
   if (p.rows.n <= 0) return cudaSuccess;
   const uint64_t BC = (uint64_t)p.rows.n * p.C;  // inputs and outputs: the launch rows
   bool ok = make_map(&maps.q, p.q, p.Hq, BC, row, row * p.Hq, 1, BM) &&
-            make_map(&maps.kc, p.k, p.Hkv, BC, row, row * p.Hkv, 1, BN) &&
-            make_map(&maps.vc, p.v, p.Hkv, BC, row, row * p.Hkv, 1, BN);
+            make_map(&maps.kc, p.k, p.Hkv, p.C, row, row * p.Hkv, 1, BN, p.rows.n) &&
+            make_map(&maps.vc, p.v, p.Hkv, p.C, row, row * p.Hkv, 1, BN, p.rows.n);
   // A kind with no heads in this layer keeps zeroed maps: no CTA reads them.
   // Retrieval buffers are addressed by storage row (packed or paged), so
   // their maps are flat; TMA coordinates are 32-bit.

@@ -82,6 +82,26 @@ def test_split_prefill_keeps_nan(cuda_lib, n, C, bad):
     assert torch.equal(out[:at], clean[:at]) and torch.equal(out[:, 4:], clean[:, 4:])
 
 
+@pytest.mark.parametrize("kv", ["fp8", "bf16", "int4"])
+@pytest.mark.parametrize("C", [5, 128, 130, 300])
+def test_prefill_rows_do_not_meet(cuda_lib, kv, C):
+    """NaN in one row's chunk stays in that row: a key tile that reaches past a
+    row's last token does not read the next row's."""
+    n = 70
+    cache = DuoCache(1, 3, 8, 2, D, kv, n + C, torch.tensor([[1, 0]]), 4, 60)
+    k, v, q = (torch.stack([_seq(10 * i + b, n + C, h) for b in range(3)]) for i, h in ((1, 2), (2, 2), (3, 8)))
+    cache.append(0, k[:, :n].contiguous(), v[:, :n].contiguous())
+    k, v, q = (x[:, n:].contiguous() for x in (k, v, q))
+    clean = cache.prefill(0, q, k, v)
+    for t in (q, k, v):
+        t[1] = NAN
+    out = cache.prefill(0, q, k, v)
+    torch.cuda.synchronize()
+    assert B.duo_poll_device_error() == 0
+    assert torch.isfinite(clean.float()).all() and out[1].isnan().all()
+    assert torch.equal(out[::2], clean[::2])
+
+
 # ------------------------------------------------------------------ decode
 
 
