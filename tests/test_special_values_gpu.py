@@ -102,6 +102,35 @@ def test_prefill_rows_do_not_meet(cuda_lib, kv, C):
     assert torch.equal(out[::2], clean[::2])
 
 
+@pytest.mark.parametrize("kv", ["fp8", "int4"])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("n,C", [(1, 5), (70, 130), (129, 300), (200, 20), (255, 1), (256, 7), (300, 129), (383, 257)])
+def test_prefill_after_a_spoilt_sequence(cuda_lib, kv, paged, n, C):
+    """Rows of a coded cache that hold NaN and infinities beside or before a
+    sequence, in its blocks, slots, pages or the next ones, do not reach its
+    pre-fill."""
+    cap = n + C + 300
+    kw = dict(pool_blocks=3 * -(-cap // 256)) if paged else {}
+    k, v, q = (torch.stack([_seq(10 * i + b, n + C, h) for b in range(3)]) for i, h in ((1, 4), (2, 4), (3, 8)))
+    hist, part = [x[:, :n].contiguous() for x in (k, v)], [x[:, n:].contiguous() for x in (q, k, v)]
+    outs = []
+    for spoilt in (False, True):
+        cache = DuoCache(1, 3, 8, 4, D, kv, cap, torch.tensor([[1, 0, 1, 0]]), 4, 500, **kw)
+        if spoilt:
+            bad = torch.full((3, cap, 4, D), NAN, dtype=BF, device="cuda")
+            bad[:, ::3] = INF
+            cache.append(0, bad, bad)
+            cache.release_rows([0, 2])
+        else:
+            cache.append_rows(0, [1], *(x[1:2] for x in hist))
+        rows = [2, 0]
+        cache.append_rows(0, rows, *(x[rows] for x in hist))
+        outs.append(cache.prefill_rows(0, rows, *(x[rows] for x in part)))
+        torch.cuda.synchronize()
+        assert B.duo_poll_device_error() == 0
+    assert torch.isfinite(outs[0].float()).all() and torch.equal(outs[0], outs[1])
+
+
 # ------------------------------------------------------------------ decode
 
 
