@@ -18,6 +18,11 @@
 //   O_X += P_X V_j    (A operand from TMEM, V read MN-major from smem)
 // S, P and O live in tensor memory (4 x 128 columns); O is rescaled in TMEM only
 // when a row's running max grows by more than 2^8 (the ratio stays exact).
+// P is bf16, V's type and the only one that a product with V takes (half a step,
+// 2^-8 of each probability; l sums them unrounded): outputs of random values
+// are off by 2.2e-3 of their norm in all, of which their own rounding to bf16
+// is 1.7e-3.  A second product with what P lost would add half of the tensor
+// work to every tile.
 // Both query tiles share every K/V tile; K/V are double buffered.
 //
 // A short chunk on a long history has few (head, query pair) items, each a

@@ -21,10 +21,14 @@
 // vectors, each lane holding the four (cos, sin) of its pairs.
 //
 // Bound: HBM, each vector read and written once.  Measured: 4096 tokens of 32
-// + 8 bf16 heads 14.4 us (5.8 TB/s, 0.89 of the copy rate), 4 x 1777 tokens of
-// 32 + 32 heads into a bf16 cache 43.5 us (0.72); short calls 2.7 us.  What is
+// + 8 bf16 heads 14.3 us (5.9 TB/s, 0.89 of the copy rate), 4 x 1777 tokens of
+// 32 + 32 heads into a bf16 cache 43.7 us (0.72); short calls 2.7 us.  What is
 // left is load latency, next to it instruction issue: 64 registers (four
-// vectors waiting, packed) let 32 warps share an SM.  Slower: a ring of
+// vectors waiting, packed) let 32 warps share an SM.  They fit the full
+// rotation of halves; the other bf16 variants spill 48 to 112 bytes a thread:
+// the same call with pairs of neighbours 17.6 us, with half the channels
+// rotated 16.5, with both 19.6.  fp32, 80 registers: 32.7, 34.3, 33.0 and 34.8
+// us for twice the bytes (0.78 to 0.73).  Slower: a ring of
 // asynchronous copies in shared memory (23.5 us at 4096 tokens when the kernel
 // took 19.4), two tokens a CTA (16.6 against 14.5), six vectors waiting (19.3).
 //
@@ -37,7 +41,7 @@
 // where codes past 240 would stand for more than fp32 holds, 240 is the
 // largest).  A power
 // of two makes the division and the expansion to bf16 exact.  8192 tokens of 4
-// retrieval heads with 32 query heads: 43 us (0.57); without queries 16.7, most
+// retrieval heads with 32 query heads: 43.3 us (0.57); without queries 15.6, most
 // of it the blocks: an angle is formed for four heads only, and each CTA's
 // set-up, loads, largest values and stores follow one another.
 #include <algorithm>
@@ -64,7 +68,8 @@ constexpr int kRing = 2;
 constexpr int kBlockThreads = 256, kRowThreads = 128;
 constexpr int threads_of(int mode) { return mode == kFp8Mode ? kBlockThreads : kRowThreads; }
 // CTAs an SM has to hold: 64 registers a thread, 80 for fp32; 72 for the
-// appends (4 x 1777 tokens of 96 vectors: 43.5 us, 45.7 with 64, 47.0 with 80);
+// appends (4 x 1777 tokens of 96 vectors: 43.5 us, 45.7 with 64, 47.0 with 80;
+// the 4-bit append spills 28 bytes so and takes 95.7, its divisions);
 // 80 for the 8-bit append, whose scale blocks spill with less (3000 tokens of 32
 // heads: 22.4 us, 28.5 with 64).
 constexpr int ctas_of(int mode, int elt) {

@@ -102,7 +102,10 @@ typedef enum duo_status {
  * alone, not on how they were split into calls.  Streaming heads hold bf16
  * rows: their ring overwrites slot by slot, which a block's scale could not
  * follow without coding old tokens anew.  Attention reads exactly what is
- * held: code * scale for full blocks, bf16 for the rest. */
+ * held: code * scale for full blocks, bf16 for the rest.  Decode: scores and
+ * sums in float32, probabilities to 16 bits or more in the product with V.
+ * Pre-fill: as DUO_BF16, probabilities rounded to bf16 (half a step, 2^-8 of
+ * each) for that product and summed in float32 before. */
 typedef enum duo_kv_dtype { DUO_F32 = 0, DUO_BF16 = 1, DUO_INT4 = 2, DUO_FP8 = 3 } duo_kv_dtype;
 #define DUO_FP8_BLOCK 32 /* tokens per scale of an 8-bit cache */
 
@@ -242,7 +245,8 @@ typedef struct duo_heads {
  * tensors' type.  The angle is a 64-bit fixed-point fraction of a turn, so that
  * far positions keep their phase: off by less than 2^-26 radian while
  * |position| * max(|inv_freq|, 8) < 2^36.  A frequency that is not finite makes
- * its pair's channels NaN. */
+ * its pair's channels NaN.  The norm's sum of squares is float32: channels
+ * beyond 2^60 overflow it (and, with norm_eps 0, vectors below 2^-60 are lost). */
 typedef struct duo_rope_desc {
   int32_t rot_dim;       /* 0 (no rotation) .. head_dim, a multiple of 16 */
   int32_t interleaved;   /* 0 or 1 */
@@ -393,6 +397,14 @@ duo_status duo_decode_attn_static(duo_cache *cache, int32_t layer, const void *q
  * exactly as given.  Key tiles are 128 rows, so a tile can cover rows past a
  * row's length (probability 0); the expansion writes zeros there, so the
  * workspace needs no initialisation.
+ * V has to be finite wherever a tile of 128 keys reaches, seen or not, since
+ * 0 * NaN is NaN: a NaN or infinity in V reaches every query of its head in
+ * the row whose tiles hold that key, earlier tokens of the chunk among them (so
+ * a padded chunk is padded with finite values).  K may hold anything where it
+ * is not seen.  A row never reads another row's chunk; on a DUO_BF16 cache
+ * the history's last tile reads the buffer's rows past the row's length too
+ * (what a released sequence left there, or, packed with a capacity that is not
+ * a multiple of 128, the next head's), which DUO_INT4 and DUO_FP8 do not.
  * Errors: DUO_ERR_CAPACITY if len + C would pass capacity in a row;
  * DUO_ERR_WORKSPACE if an INT4 or FP8 cache gets a missing or small workspace. */
 duo_status duo_prefill_attn(duo_cache *cache, int32_t layer, const void *q,
@@ -574,8 +586,8 @@ duo_status duo_test_plan_prefill(const duo_cache *cache, int32_t layer,
  * caches. */
 duo_status duo_test_force_prefill_runs(duo_cache *cache, int32_t runs);
 
-/* Read and clear the device-side error word that bounded in-kernel waits set
- * when they give up.  Synchronises the device.  Returns DUO_ERR_TIMEOUT if it
+/* Read and clear the current device's error word, which bounded in-kernel
+ * waits set when they give up.  Synchronises the device.  Returns DUO_ERR_TIMEOUT if it
  * was set, DUO_OK otherwise; *code (may be NULL) receives the raw word.
  * The outputs of a call whose wait gave up are undefined.  A decode CTA that
  * gives up still leaves an empty partial and takes its merge ticket, so the
